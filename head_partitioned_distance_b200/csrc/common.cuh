@@ -14,6 +14,7 @@ constexpr int kMaxHeads = 256;
 
 // Status codes mirrored from spa.h (kept numerically identical).
 constexpr int kStatusOk = 0;
+constexpr int kStatusInval = 1;
 constexpr int kStatusUnsupported = 2;
 constexpr int kStatusTimeout = 4;
 
@@ -87,7 +88,8 @@ __device__ __forceinline__ int head_of(const int32_t* start, int H, int r) {
 }
 
 // The library's device error word: a kernel that times out on a wait stores
-// kStatusTimeout here; spa_device_status() reads and clears it.
+// kStatusTimeout here, one that meets a device-side index out of its range
+// (a page, a position) kStatusInval; spa_device_status() reads and clears it.
 __device__ int g_spa_status;
 
 // Bounded wait on one mbarrier phase.  Returns false when the CTA aborted:

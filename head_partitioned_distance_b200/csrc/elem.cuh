@@ -1,0 +1,48 @@
+// elem.cuh -- the two 16-bit element types of the query/key norm and of the
+// paged cache: packing, unpacking, and rows of 16-byte vectors.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "ptx.cuh"
+
+namespace spa {
+
+struct Bf16 {
+  static constexpr uint32_t kMmaFormat = 1;  // tcgen05 kind::f16 operand format
+  static constexpr bool kIsBf16 = true;
+  __device__ __forceinline__ static float2 unpack(uint32_t v) { return ptx::bf16x2_to_float2(v); }
+  // round to nearest even; `lo` at the lower address
+  __device__ __forceinline__ static uint32_t pack(float lo, float hi) { return ptx::pack_bf16x2(lo, hi); }
+};
+
+struct Fp16 {
+  static constexpr uint32_t kMmaFormat = 0;
+  static constexpr bool kIsBf16 = false;
+  __device__ __forceinline__ static float2 unpack(uint32_t v) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+  __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+};
+
+template <class E>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = E::unpack(ptx::word_of(v, e));
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
+}
+
+template <class E>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
+}
+
+}  // namespace spa

@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "fwd.cuh"
+#include "norm_rope.cuh"
 #include "sched.cuh"
 #include "union.cuh"
 
@@ -667,6 +668,115 @@ int noalloc_scratch(void** out) {
   return SPA_OK;
 }
 
+// ------------------------------------------------------------ norm and rotation
+int check_dtype(int dtype) { return dtype == SPA_BF16 || dtype == SPA_FP16 ? SPA_OK : SPA_ERR_INVAL; }
+
+// Rows of a [B][H][N][d] tensor are read and written in 16-byte vectors: a
+// stride that is used (its extent is above one) is a multiple of 8 elements.
+bool vector_strides(const int64_t* s, int64_t B, int64_t H, int64_t N) {
+  return (B == 1 || s[0] % 8 == 0) && (H == 1 || s[1] % 8 == 0) && (N == 1 || s[2] % 8 == 0);
+}
+
+spa::RowStrides row_strides(const int64_t* s) { return {s[0], s[1], s[2]}; }
+
+int check_norm_rope(int64_t heads, int d, int rot, int64_t table_len, float eps, int dtype) {
+  if (check_dtype(dtype) || table_len < 1 || !std::isfinite(eps) || !(eps >= 0.f)) return SPA_ERR_INVAL;
+  if ((d != 64 && d != 128) || rot < 16 || rot > d || rot % 16 || heads > 1024) return SPA_ERR_UNSUPPORTED;
+  return SPA_OK;
+}
+
+int check_qk(int B, int Hq, int Hk, int64_t N, const int64_t* qs, const int64_t* ks) {
+  if (B < 1 || Hq < 1 || Hk < 1 || N < 1 || !qs || !ks) return SPA_ERR_INVAL;
+  if (N > 2147483647LL || (int64_t)B * N > 2147483647LL) return SPA_ERR_UNSUPPORTED;
+  return vector_strides(qs, B, Hq, N) && vector_strides(ks, B, Hk, N) ? SPA_OK : SPA_ERR_UNSUPPORTED;
+}
+
+// Heads that one lane group walks: as many as leave every SM about 2048
+// threads of lane groups, so that a token's table row is read once for many
+// heads when there are many tokens, and few tokens still fill the GPU.
+int norm_rope_heads(int64_t tokens, int heads, int d, int sms) {
+  const int64_t groups = (int64_t)sms * 2048 / (d / 8);
+  int64_t split = (groups + tokens - 1) / tokens;  // lane groups wanted per token
+  split = split < 1 ? 1 : split;
+  const int64_t per = (heads + split - 1) / split;
+  const int64_t lo = spa::kNrUnroll, hi = 4 * spa::kNrUnroll;
+  return (int)(per < lo ? lo : per > hi ? hi : per);
+}
+
+template <class E, int D, bool NB>
+int norm_rope_fwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
+  constexpr int TOK = spa::kNrThreads / (D / 8);
+  const int heads = p.Hq + p.Hk;
+  const dim3 grid((unsigned)((p.tokens + TOK - 1) / TOK), (unsigned)((heads + p.heads_per_group - 1) / p.heads_per_group));
+  spa::spa_qk_norm_rope_fwd_kernel<E, D, NB><<<grid, spa::kNrThreads, 0, s>>>(p);
+  return launch_status();
+}
+
+template <class E, int D, bool NB>
+int norm_rope_bwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
+  constexpr int TOK = spa::kNrThreads / (D / 8);
+  const int64_t chunks = (p.Hq + p.Hk + p.heads_per_group - 1) / p.heads_per_group;
+  const int64_t units = (p.tokens + TOK - 1) / TOK * chunks;
+  const int blocks = (int)(units < spa::kNrMaxBlocks ? units : spa::kNrMaxBlocks);
+  spa::spa_qk_norm_rope_bwd_kernel<E, D, NB><<<blocks, spa::kNrThreads, 0, s>>>(p);
+  int st = launch_status();
+  if (st) return st;
+  // the sum of the partials starts its launch while the last blocks finish
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32, 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, spa::spa_qk_norm_rope_dw_kernel<D>, (const float*)p.part, blocks, p.dwq, p.dwk) !=
+      cudaSuccess)
+    return SPA_ERR_CUDA;
+  return launch_status();
+}
+
+template <class E, int D, bool NB>
+int paged_append_launch(spa::AppendParams& p, cudaStream_t s) {
+  constexpr int TOK = spa::kNrThreads / (D / 8);
+  const int heads = p.Hq + 2 * p.Hk;
+  const dim3 grid((unsigned)((p.T + TOK - 1) / TOK), (unsigned)((heads + p.heads_per_group - 1) / p.heads_per_group));
+  spa::spa_paged_append_kernel<E, D, NB><<<grid, spa::kNrThreads, 0, s>>>(p);
+  return launch_status();
+}
+
+// Calls f with the element type, head size and pairing as compile-time values.
+template <template <class, int, bool> class F, class P>
+int norm_rope_dispatch(int dtype, int d, bool neighbours, P& p, cudaStream_t s) {
+  if (dtype == SPA_BF16) {
+    if (d == 64) return neighbours ? F<spa::Bf16, 64, true>::run(p, s) : F<spa::Bf16, 64, false>::run(p, s);
+    return neighbours ? F<spa::Bf16, 128, true>::run(p, s) : F<spa::Bf16, 128, false>::run(p, s);
+  }
+  if (d == 64) return neighbours ? F<spa::Fp16, 64, true>::run(p, s) : F<spa::Fp16, 64, false>::run(p, s);
+  return neighbours ? F<spa::Fp16, 128, true>::run(p, s) : F<spa::Fp16, 128, false>::run(p, s);
+}
+template <class E, int D, bool NB>
+struct NormRopeFwd {
+  static int run(spa::NormRopeParams& p, cudaStream_t s) { return norm_rope_fwd_launch<E, D, NB>(p, s); }
+};
+template <class E, int D, bool NB>
+struct NormRopeBwd {
+  static int run(spa::NormRopeParams& p, cudaStream_t s) { return norm_rope_bwd_launch<E, D, NB>(p, s); }
+};
+template <class E, int D, bool NB>
+struct PagedAppend {
+  static int run(spa::AppendParams& p, cudaStream_t s) { return paged_append_launch<E, D, NB>(p, s); }
+};
+
+bool valid_page(int page) { return page >= 16 && page <= 256 && (page & (page - 1)) == 0; }
+
+int log2_of(int page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1081,7 +1191,167 @@ int spa_device_status(void* stream) {
     if (cudaMemcpyToSymbol(spa::g_spa_status, &z, sizeof(int)) != cudaSuccess) return SPA_ERR_CUDA;
   }
   if (v == 0) return SPA_OK;
+  if (v == spa::kStatusInval) return SPA_ERR_INVAL;
   return v == spa::kStatusUnsupported ? SPA_ERR_UNSUPPORTED : SPA_ERR_TIMEOUT;
+}
+
+int spa_rope_table(float* table, int64_t length, int rot, double base, void* stream) {
+  if (!table || length < 1 || length > 2147483647LL || !std::isfinite(base) || !(base > 0.0)) return SPA_ERR_INVAL;
+  if (rot < 16 || rot > 128 || rot % 16 || !aligned(table, 16)) return SPA_ERR_UNSUPPORTED;
+  const int64_t n = length * (rot / 2), want = (n + 255) / 256;
+  int sms = 0, st;
+  if ((st = sm_count(&sms))) return st;
+  const int64_t cap = (int64_t)sms * 8;
+  spa::spa_rope_table_kernel<<<(unsigned)(want < cap ? want : cap), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<float2*>(table), n, rot / 2, std::log2(base));
+  return launch_status();
+}
+
+int spa_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk, const float* table,
+                         const int32_t* positions, void* q_out, void* k_out, int B, int Hq, int Hk, int64_t N, int d,
+                         int rot, int64_t table_len, int64_t pos_stride, const int64_t* q_strides,
+                         const int64_t* k_strides, int interleaved, float eps, int dtype, void* stream) {
+  if (!q || !k || !wq || !wk || !table || !q_out || !k_out) return SPA_ERR_INVAL;
+  int st;
+  if ((st = check_qk(B, Hq, Hk, N, q_strides, k_strides)) ||
+      (st = check_norm_rope((int64_t)Hq + Hk, d, rot, table_len, eps, dtype)))
+    return st;
+  if (!positions && N > table_len) return SPA_ERR_INVAL;
+  for (const void* t : {q, k, (const void*)wq, (const void*)wk, (const void*)table, (const void*)q_out,
+                        (const void*)k_out})
+    if (!aligned(t, 16)) return SPA_ERR_UNSUPPORTED;
+  if (!aligned(positions, 4)) return SPA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((st = sm_count(&sms))) return st;
+  spa::NormRopeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.qs = row_strides(q_strides);
+  p.ks = row_strides(k_strides);
+  p.wq = wq;
+  p.wk = wk;
+  p.table = reinterpret_cast<const float2*>(table);
+  p.pos = positions;
+  p.pos_stride = pos_stride;
+  p.table_len = table_len;
+  p.N = N;
+  p.tokens = (int64_t)B * N;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rot = rot;
+  p.heads_per_group = norm_rope_heads(p.tokens, Hq + Hk, d, sms);
+  p.eps = eps;
+  p.qo = static_cast<uint16_t*>(q_out);
+  p.ko = static_cast<uint16_t*>(k_out);
+  return norm_rope_dispatch<NormRopeFwd>(dtype, d, interleaved != 0, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t spa_qk_norm_rope_bwd_workspace_bytes(int d) {
+  if (d != 64 && d != 128) return 0;
+  return (size_t)spa::kNrMaxBlocks * 2 * (size_t)d * sizeof(float);
+}
+
+int spa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* wq,
+                         const float* wk, const float* table, const int32_t* positions, void* dq, void* dk,
+                         float* dwq, float* dwk, void* workspace, int B, int Hq, int Hk, int64_t N, int d, int rot,
+                         int64_t table_len, int64_t pos_stride, const int64_t* q_strides, const int64_t* k_strides,
+                         const int64_t* dq_strides, const int64_t* dk_strides, int interleaved, float eps, int dtype,
+                         void* stream) {
+  if (!dq_out || !dk_out || !q || !k || !wq || !wk || !table || !dq || !dk || !dwq || !dwk || !workspace)
+    return SPA_ERR_INVAL;
+  int st;
+  if ((st = check_qk(B, Hq, Hk, N, q_strides, k_strides)) || (st = check_qk(B, Hq, Hk, N, dq_strides, dk_strides)) ||
+      (st = check_norm_rope((int64_t)Hq + Hk, d, rot, table_len, eps, dtype)))
+    return st;
+  if (!positions && N > table_len) return SPA_ERR_INVAL;
+  for (const void* t : {dq_out, dk_out, q, k, (const void*)wq, (const void*)wk, (const void*)table, (const void*)dq,
+                        (const void*)dk, (const void*)workspace})
+    if (!aligned(t, 16)) return SPA_ERR_UNSUPPORTED;
+  if (!aligned(positions, 4) || !aligned(dwq, 4) || !aligned(dwk, 4)) return SPA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((st = sm_count(&sms))) return st;
+  spa::NormRopeParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.qs = row_strides(q_strides);
+  p.ks = row_strides(k_strides);
+  p.wq = wq;
+  p.wk = wk;
+  p.table = reinterpret_cast<const float2*>(table);
+  p.pos = positions;
+  p.pos_stride = pos_stride;
+  p.table_len = table_len;
+  p.N = N;
+  p.tokens = (int64_t)B * N;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rot = rot;
+  p.heads_per_group = norm_rope_heads(p.tokens, Hq + Hk, d, sms);
+  p.eps = eps;
+  p.dqo = static_cast<const uint16_t*>(dq_out);
+  p.dko = static_cast<const uint16_t*>(dk_out);
+  p.dq = static_cast<uint16_t*>(dq);
+  p.dk = static_cast<uint16_t*>(dk);
+  p.dqs = row_strides(dq_strides);
+  p.dks = row_strides(dk_strides);
+  p.part = static_cast<float*>(workspace);
+  p.dwq = dwq;
+  p.dwk = dwk;
+  return norm_rope_dispatch<NormRopeBwd>(dtype, d, interleaved != 0, p, static_cast<cudaStream_t>(stream));
+}
+
+int spa_paged_append(const void* q, const void* k, const void* v, const float* wq, const float* wk,
+                     const float* table, const int32_t* cu_q, const int32_t* kv_len, const int32_t* page_table,
+                     void* q_out, void* k_pages, void* v_pages, int B, int T, int Hq, int Hk, int d, int64_t pages,
+                     int page, int width, int rot, int64_t table_len, const int64_t* q_strides,
+                     const int64_t* k_strides, const int64_t* v_strides, int interleaved, float eps, int dtype,
+                     void* stream) {
+  int st;
+  if (B < 1 || T < 0 || Hq < 1 || Hk < 1 || pages < 1 || width < 1 || !q_strides || !k_strides || !v_strides)
+    return SPA_ERR_INVAL;
+  if ((st = check_norm_rope((int64_t)Hq + 2LL * Hk, d, rot, table_len, eps, dtype))) return st;
+  if (B > 65535 || !valid_page(page)) return SPA_ERR_UNSUPPORTED;
+  if (T == 0) return SPA_OK;
+  if (!q || !k || !v || !wq || !wk || !table || !cu_q || !kv_len || !page_table || !q_out || !k_pages || !v_pages)
+    return SPA_ERR_INVAL;
+  for (const void* t : {q, k, v, (const void*)wq, (const void*)wk, (const void*)table, (const void*)q_out,
+                        (const void*)k_pages, (const void*)v_pages})
+    if (!aligned(t, 16)) return SPA_ERR_UNSUPPORTED;
+  if (!aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(page_table, 4)) return SPA_ERR_UNSUPPORTED;
+  const int64_t qs[3] = {0, q_strides[1], q_strides[0]}, ks[3] = {0, k_strides[1], k_strides[0]},
+                vs[3] = {0, v_strides[1], v_strides[0]};
+  if (!vector_strides(qs, 1, Hq, T) || !vector_strides(ks, 1, Hk, T) || !vector_strides(vs, 1, Hk, T))
+    return SPA_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((st = sm_count(&sms))) return st;
+  spa::AppendParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.qs = row_strides(qs);
+  p.ks = row_strides(ks);
+  p.vs = row_strides(vs);
+  p.wq = wq;
+  p.wk = wk;
+  p.table = reinterpret_cast<const float2*>(table);
+  p.table_len = table_len;
+  p.cu_q = cu_q;
+  p.kv_len = kv_len;
+  p.page_table = page_table;
+  p.qo = static_cast<uint16_t*>(q_out);
+  p.k_pages = static_cast<uint16_t*>(k_pages);
+  p.v_pages = static_cast<uint16_t*>(v_pages);
+  p.pages = pages;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.rot = rot;
+  p.width = width;
+  p.page_shift = log2_of(page);
+  p.heads_per_group = norm_rope_heads(T, Hq + 2 * Hk, d, sms);
+  p.eps = eps;
+  return norm_rope_dispatch<PagedAppend>(dtype, d, interleaved != 0, p, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

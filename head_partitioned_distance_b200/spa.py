@@ -9,6 +9,7 @@ library reports an error.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,6 +29,7 @@ _vp = ctypes.c_void_p
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _u8p = ctypes.POINTER(ctypes.c_uint8)
 _i64 = ctypes.c_int64
+_i64p = ctypes.POINTER(ctypes.c_int64)
 _int = ctypes.c_int
 _f32 = ctypes.c_float
 
@@ -68,6 +70,14 @@ EXPORTS = {
     "spa_tile_classes_device": ([_i64, _int, _i32p, _i32p, _int, _int, _vp, _vp], _int),
     "spa_debug_wait_timeout": ([_i64, _vp], _int),
     "spa_device_status": ([_vp], _int),
+    "spa_rope_table": ([_vp, _i64, _int, ctypes.c_double, _vp], _int),
+    "spa_qk_norm_rope_fwd": ([_vp] * 8 + [_int, _int, _int, _i64, _int, _int, _i64, _i64, _i64p, _i64p, _int, _f32,
+                                          _int, _vp], _int),
+    "spa_qk_norm_rope_bwd_workspace_bytes": ([_int], ctypes.c_size_t),
+    "spa_qk_norm_rope_bwd": ([_vp] * 13 + [_int, _int, _int, _i64, _int, _int, _i64, _i64, _i64p, _i64p, _i64p, _i64p,
+                                           _int, _f32, _int, _vp], _int),
+    "spa_paged_append": ([_vp] * 12 + [_int, _int, _int, _int, _int, _i64, _int, _int, _int, _i64, _i64p, _i64p, _i64p,
+                                       _int, _f32, _int, _vp], _int),
 }
 for _name, (_args, _res) in EXPORTS.items():
     _fn = getattr(_lib, _name)
@@ -630,3 +640,252 @@ def spa_attn_union_add_grads(dq, dk, dv, dq2, dk2, dv2, stream=None):
                                          dk2.data_ptr(), dv2.data_ptr(), B, H, N, d, _stream_ptr(stream)),
            "spa_attn_union_add_grads")
     return dq, dk, dv
+
+
+# ------------------------------------------------------------- norm and rotation
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # spa_dtype_t
+
+
+def _on(device):
+    """Makes `device` current for a launch (the launch goes to the current device)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_on(device, stream):
+    return _vp((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in DTYPES or not t.is_cuda:
+        raise ValueError(f"{name}: expected CUDA bfloat16 or float16 tensor, got {t.dtype} on {t.device}")
+    return DTYPES[t.dtype]
+
+
+def _need_on(t, shape, dtype, device, name):
+    """A contiguous tensor of this shape and type on `device`."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _vector_rows(t) -> bool:
+    """Rows (the last dimension) contiguous and every row 16-byte aligned."""
+    return t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and \
+        all(s % 8 == 0 or n == 1 for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+
+
+def _need_rows(t, shape, dtype, device, name):
+    """A tensor of this shape and type on `device`, its rows readable in 16-byte vectors."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if not _vector_rows(t):
+        raise ValueError(f"{name}: the last dimension must be contiguous, rows 16-byte aligned and the other strides "
+                         f"multiples of 8, got strides {t.stride()}")
+
+
+def _strides(t):
+    n = t.dim() - 1
+    return (ctypes.c_int64 * n)(*t.stride()[:n])
+
+
+def _rope_args(table, positions, B, N, device):
+    """(rot, positions pointer, stride between batches) of a checked table and positions."""
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table: expected [length, rot / 2, 2] (rope_table), got {tuple(table.shape)}")
+    _need_on(table, table.shape, torch.float32, device, "table")
+    rot = 2 * table.shape[1]
+    if positions is None:
+        if N > table.shape[0]:
+            raise ValueError(f"table: {N} rows need positions up to {N - 1}, the table has {table.shape[0]}")
+        return rot, None, 0
+    if positions.dtype != torch.int32 or positions.device != device or tuple(positions.shape) not in ((N,), (B, N)) \
+            or (N > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions: expected int32 [{N}] or [{B}, {N}] on {device}, rows contiguous, got "
+                         f"{positions.dtype} {tuple(positions.shape)} on {positions.device}")
+    return rot, positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0
+
+
+def _qk_dims(q, k):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k are [B, H, N, d]")
+    B, Hq, N, d = q.shape
+    return B, Hq, k.shape[1], N, d
+
+
+def spa_rope_table(table, base: float, stream=None):
+    """Fill table [length, rot / 2, 2] fp32 with (cos, sin) of pos * base^(-2 i / rot)."""
+    if table.dim() != 3 or table.shape[2] != 2 or not table.is_cuda:
+        raise ValueError(f"table: expected CUDA tensor [length, rot / 2, 2], got {tuple(table.shape)} on {table.device}")
+    _need_on(table, table.shape, torch.float32, table.device, "table")
+    with _on(table.device):
+        _check(_lib.spa_rope_table(table.data_ptr(), table.shape[0], 2 * table.shape[1], base,
+                                   _stream_on(table.device, stream)), "spa_rope_table")
+    return table
+
+
+def rope_table(length: int, rot: int, base: float = 10000.0, device=None):
+    """The rotation's table for positions [0, length) and rot rotated columns."""
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return spa_rope_table(torch.empty((length, rot // 2, 2), dtype=torch.float32, device=device), base)
+
+
+def spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, q_out, k_out, positions=None, eps: float = 1e-6,
+                         interleaved: bool = False, stream=None):
+    """q_out, k_out = the normed and rotated q [B, Hq, N, d], k [B, Hk, N, d]
+    (bf16 or fp16, any strides of whole 16-byte vectors); see spa.h."""
+    B, Hq, Hk, N, d = _qk_dims(q, k)
+    dt, dev = _dtype_code(q, "q"), q.device
+    _need_rows(q, (B, Hq, N, d), q.dtype, dev, "q")
+    _need_rows(k, (B, Hk, N, d), q.dtype, dev, "k")
+    _need_on(q_out, (B, Hq, N, d), q.dtype, dev, "q_out")
+    _need_on(k_out, (B, Hk, N, d), q.dtype, dev, "k_out")
+    _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
+    _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
+    rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
+    with _on(dev):
+        _check(_lib.spa_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
+                                         table.data_ptr(), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d,
+                                         rot, table.shape[0], pos_stride, _strides(q), _strides(k), int(interleaved),
+                                         eps, dt, _stream_on(dev, stream)), "spa_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def spa_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    return int(_lib.spa_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+def spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk, dq_weight, dk_weight, workspace,
+                         positions=None, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Gradients of sum(q_out * dq_out) + sum(k_out * dk_out): writes dq, dk (any
+    strides of whole 16-byte vectors) and dq_weight, dk_weight (fp32 [d]).
+    workspace: CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes."""
+    B, Hq, Hk, N, d = _qk_dims(q, k)
+    dt, dev = _dtype_code(q, "q"), q.device
+    for t, H, n in ((q, Hq, "q"), (k, Hk, "k"), (dq, Hq, "dq"), (dk, Hk, "dk")):
+        _need_rows(t, (B, H, N, d), q.dtype, dev, n)
+    _need_on(dq_out, (B, Hq, N, d), q.dtype, dev, "dq_out")
+    _need_on(dk_out, (B, Hk, N, d), q.dtype, dev, "dk_out")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        _need_on(t, (d,), torch.float32, dev, n)
+    if workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < spa_qk_norm_rope_bwd_workspace_bytes(d):
+        raise ValueError("workspace: contiguous CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes")
+    rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
+    with _on(dev):
+        _check(_lib.spa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                         q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), pos,
+                                         dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(),
+                                         workspace.data_ptr(), B, Hq, Hk, N, d, rot, table.shape[0], pos_stride,
+                                         _strides(q), _strides(k), _strides(dq), _strides(dk), int(interleaved), eps,
+                                         dt, _stream_on(dev, stream)), "spa_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6,
+                         interleaved: bool = False):
+    """Allocate q_out / k_out (contiguous) and run spa_qk_norm_rope_fwd."""
+    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    return spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, qo, ko, positions, eps, interleaved)
+
+
+def _grad_like(x):
+    """An empty gradient of x [B, H, N, d], dense and in x's order of heads and rows."""
+    B, H, N, d = x.shape
+    if x.stride(1) < x.stride(2):
+        return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
+    return torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6,
+                          interleaved: bool = False):
+    """Allocate dq / dk / dq_weight / dk_weight / workspace and run spa_qk_norm_rope_bwd."""
+    d = q.shape[-1]
+    dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+    ws = torch.empty(max(spa_qk_norm_rope_bwd_workspace_bytes(d) // 4, 1), dtype=torch.float32, device=q.device)
+    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, _grad_like(q), _grad_like(k), dw[0],
+                                dw[1], ws, positions, eps, interleaved)
+
+
+class QKNormRopeFunction(torch.autograd.Function):
+    """Norm and rotation of queries and keys as an autograd function."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, table, positions, eps, interleaved):
+        q, k = (x if _vector_rows(x) else x.contiguous() for x in (q, k))
+        ctx.save_for_backward(q, k, q_weight, k_weight, table, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
+        grads = qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight, table,
+                                      positions, ctx.eps, ctx.interleaved)
+        return (*grads, None, None, None, None)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6, interleaved: bool = False):
+    """RMS norm of every query and key head with its weight, then the rotary
+    position rotation: what q [B, Hq, N, d] and k [B, Hk, N, d] pass through
+    before spattention.  Differentiable in q, k and the weights.  q and k may
+    be views of a token-major projection; the outputs are contiguous.  Weights
+    of another type are used in fp32.  table: rope_table(...); positions:
+    int32 [N] or [B, N], or None for 0 .. N - 1."""
+    return QKNormRopeFunction.apply(q, k, q_weight.float(), k_weight.float(), table, positions, eps, interleaved)
+
+
+# ------------------------------------------------------------- paged cache
+def _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, dtype, device):
+    """Checks the cache's tensors; returns (B, pages, page, width)."""
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages and v_pages are [pages, Hk, page, d], page_table is [B, width]")
+    pages, page = k_pages.shape[0], k_pages.shape[2]
+    B, width = page_table.shape
+    _need_on(k_pages, (pages, Hk, page, d), dtype, device, "k_pages")
+    _need_on(v_pages, (pages, Hk, page, d), dtype, device, "v_pages")
+    _need_on(page_table, (B, width), torch.int32, device, "page_table")
+    _need_on(cu_q, (B + 1,), torch.int32, device, "cu_q")
+    _need_on(kv_len, (B,), torch.int32, device, "kv_len")
+    return B, pages, page, width
+
+
+def spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, q_out, k_pages, v_pages,
+                     eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """The new tokens' q [T, Hq, d] and k [T, Hk, d] normed and rotated at their
+    positions; q to q_out, k and v to their places in the pages (spa.h)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v are [T, H, d]")
+    T, Hq, d = q.shape
+    Hk = k.shape[1]
+    dt, dev = _dtype_code(q, "q"), q.device
+    _need_rows(q, (T, Hq, d), q.dtype, dev, "q")
+    _need_rows(k, (T, Hk, d), q.dtype, dev, "k")
+    _need_rows(v, (T, Hk, d), q.dtype, dev, "v")
+    _need_on(q_out, (T, Hq, d), q.dtype, dev, "q_out")
+    _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
+    _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
+    B, pages, page, width = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, q.dtype, dev)
+    rot, _, _ = _rope_args(table, None, 1, 0, dev)
+    with _on(dev):
+        _check(_lib.spa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_weight.data_ptr(),
+                                     k_weight.data_ptr(), table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+                                     page_table.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                     B, T, Hq, Hk, d, pages, page, width, rot, table.shape[0], _strides(q),
+                                     _strides(k), _strides(v), int(interleaved), eps, dt, _stream_on(dev, stream)),
+               "spa_paged_append")
+    return q_out
+
+
+def paged_append(q, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q_weight, k_weight, table, eps: float = 1e-6,
+                 interleaved: bool = False, out=None):
+    """Norm and rotate the new tokens' queries and keys, store keys and values in
+    the paged cache, return the queries (allocated unless given as out; rows
+    behind the last sequence are not written)."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    return spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, out, k_pages, v_pages, eps,
+                            interleaved)

@@ -432,12 +432,118 @@ SPA_API int spa_debug_wait_timeout(int64_t limit_ns, void* stream);
 /*
  * Synchronises `stream` and returns the library's device error word, then
  * clears it: SPA_OK; SPA_ERR_TIMEOUT when a kernel gave up on a wait (the
- * kernel then wrote incomplete outputs and released its tensor memory); or
- * SPA_ERR_UNSUPPORTED when a kernel found its dynamic shared memory too
- * small for its tiles after aligning the base to 1024 bytes (it returned
- * without writing its outputs).
+ * kernel then wrote incomplete outputs and released its tensor memory); 
+ * SPA_ERR_INVAL when a kernel met an index in device memory that lies outside
+ * its range (a page or position of the paged calls, which say what they do
+ * with it); or SPA_ERR_UNSUPPORTED when a kernel found its dynamic shared
+ * memory too small for its tiles after aligning the base to 1024 bytes (it
+ * returned without writing its outputs).
  */
 SPA_API int spa_device_status(void* stream);
+
+/* Element type of the 16-bit tensors of the calls below. */
+typedef enum spa_dtype { SPA_BF16 = 0, SPA_FP16 = 1 } spa_dtype_t;
+
+/*
+ * Norm and rotation of queries and keys, the step between a layer's
+ * projections and its attention.  For each head row x (d values) at position
+ * pos, with a learned weight w (one for the query heads, one for the key
+ * heads):
+ *   n = x / sqrt(mean(x^2) + eps),   y = R(pos) (w * n),
+ * where R(pos) turns rot / 2 pairs of the first rot columns: pair i by the
+ * angle whose (cos, sin) is table[pos][i]; columns from rot on are not turned.
+ * The pairs are columns (i, i + rot / 2), or with interleaved != 0 (2i, 2i + 1).
+ *   q, k:      DEVICE, [B][Hq][N][d] and [B][Hk][N][d] of type `dtype`, read
+ *              through strides: q_strides, k_strides are HOST arrays of the
+ *              element strides {batch, head, row}; the d values of a row are
+ *              contiguous.  So q and k may be parts of a token-major
+ *              [B][N][heads][d] projection.  Hq and Hk need not be equal.
+ *   wq, wk:    DEVICE fp32 [d]
+ *   table:     DEVICE fp32 [table_len][rot / 2][2], see spa_rope_table
+ *   positions: DEVICE int32, position of row (b, n) at b * pos_stride + n
+ *              (pos_stride 0: one row of N positions for every batch), or
+ *              NULL for position n.  A row whose position lies outside
+ *              [0, table_len) gets y = 0 and passes no gradient.
+ *   q_out, k_out: DEVICE, [B][Hq][N][d], [B][Hk][N][d] contiguous, the layout
+ *              of spa_attn_fwd; must not overlap the inputs
+ * One launch, asynchronous on `stream`.  Sums are fp32, outputs are rounded
+ * once.  SPA_ERR_INVAL for null pointers, sizes < 1, eps not finite or < 0,
+ * an unknown dtype, N > table_len without positions; SPA_ERR_UNSUPPORTED for d not in {64, 128}, rot not a
+ * multiple of 16 in [16, d], Hq + Hk > 1024, B * N > 2^31 - 1, tensors not
+ * 16-byte aligned (positions: 4) and strides that are not multiples of 8.
+ */
+SPA_API int spa_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const float* wk, const float* table,
+                                 const int32_t* positions, void* q_out, void* k_out, int B, int Hq, int Hk,
+                                 int64_t N, int d, int rot, int64_t table_len, int64_t pos_stride,
+                                 const int64_t* q_strides, const int64_t* k_strides, int interleaved, float eps,
+                                 int dtype, void* stream);
+
+/*
+ * Its backward.  With g = R(pos)^T dy, r = 1 / sqrt(mean(x^2) + eps), n = r x:
+ *   dw = sum over rows and heads of g * n,   dx = r (g * w - n mean(g * w * n)).
+ *   dq_out, dk_out: gradients of q_out, k_out, contiguous as those
+ *   dq, dk:         outputs, written through dq_strides, dk_strides (rules of
+ *                   the inputs' strides; no two elements may share memory)
+ *   dwq, dwk:       outputs, fp32 [d]
+ *   workspace:      DEVICE buffer of spa_qk_norm_rope_bwd_workspace_bytes(d)
+ *                   bytes, 16-byte aligned, caller-owned, overwritten
+ * The norm is formed again from q and k.  Two launches; sums over rows are
+ * added in a fixed order, so results are the same from call to call.
+ */
+SPA_API size_t spa_qk_norm_rope_bwd_workspace_bytes(int d);
+SPA_API int spa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                 const float* wq, const float* wk, const float* table, const int32_t* positions,
+                                 void* dq, void* dk, float* dwq, float* dwk, void* workspace, int B, int Hq, int Hk,
+                                 int64_t N, int d, int rot, int64_t table_len, int64_t pos_stride,
+                                 const int64_t* q_strides, const int64_t* k_strides, const int64_t* dq_strides,
+                                 const int64_t* dk_strides, int interleaved, float eps, int dtype, void* stream);
+
+/*
+ * The rotation's table: table[pos][i] = (cos, sin) of pos * base^(-2 i / rot)
+ * for 0 <= pos < length, 0 <= i < rot / 2; the angle and its functions are
+ * formed in fp64 and rounded to fp32 once, so far positions lose nothing.
+ *   table: DEVICE fp32 [length][rot / 2][2], 16-byte aligned
+ * SPA_ERR_INVAL for a null table, length outside [1, 2^31 - 1] or base not
+ * finite and > 0;
+ * SPA_ERR_UNSUPPORTED for rot not a positive multiple of 16 or above 128.
+ */
+SPA_API int spa_rope_table(float* table, int64_t length, int rot, double base, void* stream);
+
+/*
+ * Paged cache.  Keys and values of many sequences live in pages of `page`
+ * positions: k_pages, v_pages are DEVICE tensors [pages][Hk][page][d] of type
+ * `dtype`, and row b of page_table (DEVICE int32 [B][width]) names the pages
+ * of sequence b in order: position j is row j % page of page
+ * page_table[b][j / page].  A step brings new tokens, packed sequence after
+ * sequence: token rows [cu_q[b], cu_q[b + 1]) belong to sequence b (cu_q:
+ * DEVICE int32 [B + 1], non-decreasing; a sequence may have none), and
+ * kv_len[b] (DEVICE int32 [B]) counts its positions with the new tokens
+ * included, so that its new token rows stand at positions
+ * kv_len[b] - (cu_q[b + 1] - cu_q[b]) .. kv_len[b] - 1.  Token rows from
+ * cu_q[B] up to T belong to no sequence; what the outputs hold there stays.
+ * page is a power of two from 16 to 256.
+ */
+
+/*
+ * The new tokens' queries and keys normed and rotated as in
+ * spa_qk_norm_rope_fwd, at their positions; the queries written to q_out, the
+ * keys and the values (copied) to their places in the cache.
+ *   q, k, v:   DEVICE [T][Hq][d], [T][Hk][d], [T][Hk][d] through the HOST
+ *              element strides {token, head} q_strides, k_strides, v_strides
+ *   q_out:     DEVICE [T][Hq][d] contiguous
+ * A token whose position lies outside the table or the page table's width, or
+ * whose page number lies outside [0, pages), gets a zero q_out row and no
+ * place in the cache, and spa_device_status reports SPA_ERR_INVAL.  Two tokens
+ * must not share a place.  One launch; T = 0 launches nothing.  Errors as
+ * spa_qk_norm_rope_fwd, and SPA_ERR_UNSUPPORTED for a page size outside the
+ * rule above, Hq + 2 Hk > 1024 or B > 65535.
+ */
+SPA_API int spa_paged_append(const void* q, const void* k, const void* v, const float* wq, const float* wk,
+                             const float* table, const int32_t* cu_q, const int32_t* kv_len,
+                             const int32_t* page_table, void* q_out, void* k_pages, void* v_pages, int B, int T,
+                             int Hq, int Hk, int d, int64_t pages, int page, int width, int rot, int64_t table_len,
+                             const int64_t* q_strides, const int64_t* k_strides, const int64_t* v_strides,
+                             int interleaved, float eps, int dtype, void* stream);
 
 #ifdef __cplusplus
 }
