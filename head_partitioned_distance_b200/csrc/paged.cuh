@@ -1,0 +1,614 @@
+// paged.cuh -- attention of new tokens over a paged cache, each head over its
+// own band of causal distances: the work list shared by its kernels, the
+// kernel for few rows per sequence (single tokens above all), and the merge
+// of rows whose keys were split.  The kernel for many rows is in paged_long.cuh.
+//
+// Row r of sequence b stands at position p = kv_len[b] - n_b + r and attends
+// to the keys j < kv_len[b] with lo_h <= p - j < hi_h ("Making Every Head
+// Count", Figure 1 caption, the bands; softmax over the permitted set: "Story
+// of Attention -- Part 4", section 1).
+//
+// Work list.  An item is (sequence, head group, row block); a head group is
+// `group` query heads that share a key/value head and, when group > 1, one
+// band, so that each key is fetched once for all of them.  An item costs as
+// many steps as it has key tiles.  All items laid end to end form one line of
+// steps that the CTAs cut into equal runs: sequences of any mixture of lengths
+// load every SM alike, and a long sequence with few rows is spread over many
+// SMs.  An item that a cut divides leaves one partial (fp32 o, running max and
+// sum) per run, which the merge kernel joins; the others write their rows
+// directly.  Every CTA derives its run from the lengths on the device, so the
+// host needs none of them and a captured call follows them.
+#pragma once
+
+#include "common.cuh"
+#include "elem.cuh"
+
+namespace spa {
+
+struct PagedParams {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  const uint16_t* q;  // [T][Hq][d]
+  uint16_t* o;        // [T][Hq][d]
+  float* lse;         // [T][Hq]
+  int32_t* desc;      // per CTA: item it began and did not finish (or -1), CTAs that follow
+  float* part;        // two partial slots per CTA
+  int64_t pages;
+  int B, T, Hq, max_q;
+  int group;          // query heads per item
+  int ng;             // head groups: Hq / group
+  int kv_div;         // head groups per key/value head
+  int Hk;
+  int nblk;           // row blocks per (sequence, head group)
+  int blk_tokens;     // tokens per row block
+  int width, page_shift;
+  int min_run;        // steps per CTA, at least
+  int max_split;      // runs an item is cut into, about
+  float scale_log2;
+  int32_t lo[kMaxHeads];  // per head group
+  int32_t hi[kMaxHeads];
+};
+
+struct PagedItem {
+  int b, hg;
+  int row0;      // first token row
+  int tokens;    // token rows; 0: nothing to do
+  int64_t pos0;  // position of the first
+  int64_t jlo, jhi;  // keys that some row attends to (jhi < jlo: none)
+  int64_t kv;    // keys the sequence has (and the page table can name)
+  int t0;        // first key tile
+  int cost;      // steps; an item without keys takes one
+};
+
+template <int TK>
+__device__ __forceinline__ PagedItem paged_item(const PagedParams& p, int b, int hg, int blk) {
+  PagedItem it;
+  it.b = b;
+  it.hg = hg;
+  const int c0 = p.cu_q[b], n_all = p.cu_q[b + 1] - c0;
+  const int len = p.kv_len[b];
+  const int n = (c0 < 0 || c0 >= p.T) ? 0 : min(min(n_all, p.max_q), p.T - c0);
+  const int first = blk * p.blk_tokens;
+  it.row0 = c0 + first;
+  it.tokens = max(0, min(p.blk_tokens, n - first));
+  it.pos0 = (int64_t)len - n_all + first;
+  it.kv = min64(max(len, 0), (int64_t)p.width << p.page_shift);
+  it.jlo = max64(0, it.pos0 - p.hi[hg] + 1);
+  it.jhi = min64(it.pos0 + it.tokens - 1 - p.lo[hg], it.kv - 1);
+  const bool any = it.tokens > 0 && it.jhi >= it.jlo;
+  it.t0 = any ? (int)(it.jlo / TK) : 0;
+  it.cost = it.tokens == 0 ? 0 : any ? (int)(it.jhi / TK) - it.t0 + 1 : 1;
+  return it;
+}
+
+template <int TK>
+__device__ __forceinline__ PagedItem paged_item_at(const PagedParams& p, int item) {
+  const int blk = item % p.nblk, rest = item / p.nblk;
+  return paged_item<TK>(p, rest / p.ng, rest % p.ng, blk);
+}
+
+// This CTA's run of steps.
+struct PagedRun {
+  long long s0, s1;  // [s0, s1) of the line
+  long long run;     // steps per CTA
+  int item, off;     // item that holds step s0, and the steps of it before s0
+};
+
+struct PagedPlanSmem {
+  long long sum[32];
+  int most[32];
+  PagedRun run;
+};
+
+// Called by all NT threads of the CTA; ends with a barrier.
+template <int TK, int NT>
+__device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlanSmem& sm) {
+  const int items = p.B * p.ng * p.nblk;
+  const int per = (items + NT - 1) / NT;
+  const int i0 = min((int)threadIdx.x * per, items), i1 = min(i0 + per, items);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  long long mine = 0;
+  int most = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int c = paged_item_at<TK>(p, i).cost;
+    mine += c;
+    most = max(most, c);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += v;
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
+  }
+  if (lane == 31) sm.sum[warp] = incl;
+  if (lane == 0) sm.most[warp] = most;
+  if (threadIdx.x == 0) {
+    sm.run.item = items;
+    sm.run.off = 0;
+  }
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  most = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += sm.sum[w];
+    total += sm.sum[w];
+    most = max(most, sm.most[w]);
+  }
+  long long run = (total + gridDim.x - 1) / gridDim.x;
+  run = max(run, (long long)((most + p.max_split - 1) / p.max_split));
+  run = max(run, (long long)p.min_run);
+  const long long s0 = min(run * blockIdx.x, total), s1 = min(s0 + run, total);
+  if (s0 < s1 && before <= s0 && s0 < before + mine) {
+    long long at = before;
+    for (int i = i0; i < i1; ++i) {
+      const int c = paged_item_at<TK>(p, i).cost;
+      if (at + c > s0) {
+        sm.run.item = i;
+        sm.run.off = (int)(s0 - at);
+        break;
+      }
+      at += c;
+    }
+  }
+  if (threadIdx.x == 0) {
+    sm.run.s0 = s0;
+    sm.run.s1 = s1;
+    sm.run.run = run;
+  }
+  __syncthreads();
+}
+
+// The pieces of a CTA's run, in order: tiles [t0, t1) of one item each.
+template <int TK>
+struct PagedWalk {
+  const PagedParams& p;
+  long long left;
+  int item, off;
+  PagedItem it;
+  int t0, t1;     // key tiles of this piece (none for an item without keys)
+  int len;        // steps
+  bool whole;     // the piece is the whole item
+  bool begins;    // it holds the item's first step
+  __device__ __forceinline__ PagedWalk(const PagedParams& pp, const PagedRun& r)
+      : p(pp), left(r.s1 - r.s0), item(r.item - 1), off(r.off) {}
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    do {
+      it = paged_item_at<TK>(p, ++item);
+    } while (it.cost == 0);
+    len = (int)min((long long)(it.cost - off), left);
+    whole = len == it.cost;
+    begins = off == 0;
+    t0 = it.t0 + off;
+    t1 = it.jhi < it.jlo ? t0 : t0 + len;
+    left -= len;
+    off = 0;
+    return true;
+  }
+};
+
+// Partial of `rows` rows: o [rows][d], then the maxima (base 2) and the sums.
+__host__ __device__ constexpr int64_t paged_slot_floats(int rows, int d) { return (int64_t)rows * (d + 2); }
+
+// A CTA's partials: a piece that ends an item begun by an earlier CTA (or lies
+// inside it) goes to slot 2c, one that begins an item to slot 2c + 1.
+__device__ __forceinline__ float* paged_slot(const PagedParams& p, int cta, bool begins, int rows, int d) {
+  return p.part + (2 * (int64_t)cta + (begins ? 1 : 0)) * paged_slot_floats(rows, d);
+}
+
+// What the merge has to do for the item this CTA began (one thread).
+__device__ __forceinline__ void paged_describe(const PagedParams& p, int item, int followers) {
+  p.desc[2 * blockIdx.x] = item;
+  p.desc[2 * blockIdx.x + 1] = followers;
+}
+
+// Token row and head of row r of an item.
+__device__ __forceinline__ int64_t paged_row(const PagedParams& p, const PagedItem& it, int r) {
+  return ((int64_t)it.row0 + r / p.group) * p.Hq + it.hg * p.group + r % p.group;
+}
+
+// ------------------------------------------------------------------ few rows
+// Items of at most 16 rows (new tokens x heads of the group).  Bound by the
+// bytes of the keys and values: each CTA streams 64-key tiles of K and V into
+// a shared-memory ring by TMA, page by page, and four warps share a tile, 16
+// keys each, with their own running max and sum; both products are m16n8k16
+// warp matrix instructions (the rows padded to 16: the arithmetic is a fifth
+// of the time the bytes take, and single rows need no tcgen05 tile of 128).
+// P stays in registers, which its accumulator layout lets serve as the A
+// operand.  The four warps' results meet at the end of a piece.
+template <int D>
+struct PagedShortCfg {
+  static constexpr int TK = 64, ROWS = 16, WARPS = 4, NTHREADS = 160, CTAS_PER_SM = 2;
+  static constexpr int NS = D == 128 ? 3 : 6;  // 96 KB of tiles in flight per CTA
+  static constexpr uint32_t KV_BYTES = TK * D * 2, STAGE_BYTES = 2 * KV_BYTES;
+  static constexpr uint32_t OFF_RED = NS * STAGE_BYTES;          // [WARPS][4 rows][D] fp32
+  static constexpr uint32_t OFF_ML = OFF_RED + WARPS * 4 * D * 4;  // [2][WARPS][ROWS] fp32
+  static constexpr uint32_t OFF_PLAN = OFF_ML + 2 * WARPS * ROWS * 4;
+  static constexpr uint32_t OFF_BAR = OFF_PLAN + 512;
+  static constexpr uint32_t USED = OFF_BAR + 256;
+  static constexpr uint32_t SMEM_BYTES = USED + 1024;  // alignment slack
+  static_assert(sizeof(PagedPlanSmem) <= 512, "plan space");
+  static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
+};
+
+struct PagedShortBars {
+  uint64_t full[6], empty[6];
+  int abort;
+};
+
+template <class E>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (E::kIsBf16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Page numbers of one item's key tiles, 32 boxes of `BOX` keys ahead in the
+// producer warp's registers (lane i holds box base + i), so that the page
+// table's latency is paid once per 32 boxes.  Boxes that hold no key any row
+// attends to give -1 and are never looked up; so do page numbers out of range,
+// which also raise the status word.  A load at page -1 lies outside the tensor
+// and fills with zeros.
+struct PagedPages {
+  int64_t base = 0;
+  int id = -1;
+  // page of box `box + which`; the tile has the boxes [box, box + n), n <= 32
+  __device__ __forceinline__ int get(const PagedParams& p, const PagedItem& it, int64_t box, int box_shift, int n,
+                                     int which, bool fresh) {
+    const int lane = threadIdx.x % 32;
+    if (fresh || box < base || box + n > base + 32) {
+      base = box;
+      const int64_t j = (box + lane) << box_shift;
+      id = -1;
+      if (j <= it.jhi && j + (1 << box_shift) > it.jlo) {
+        id = p.page_table[(int64_t)it.b * p.width + (j >> p.page_shift)];
+        if (id < 0 || id >= p.pages) {
+          id = -1;
+          atomicExch(&g_spa_status, kStatusInval);
+        }
+      }
+    }
+    return __shfl_sync(0xffffffffu, id, (int)(box - base) + which);
+  }
+};
+
+template <class E, int D>
+__global__ void __launch_bounds__(160, 2)
+    spa_paged_short_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ PagedParams p) {
+  using C = PagedShortCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  if (!smem_fits(smem_raw, smem, C::USED)) return;
+  PagedShortBars* bars = reinterpret_cast<PagedShortBars*>(smem + C::OFF_BAR);
+  PagedPlanSmem& plan = *reinterpret_cast<PagedPlanSmem*>(smem + C::OFF_PLAN);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      ptx::mbar_init(&bars->full[s], 1);
+      ptx::mbar_init(&bars->empty[s], C::WARPS);
+    }
+    bars->abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+  }
+  paged_plan<C::TK, C::NTHREADS>(p, plan);
+  // the merge kernel may start its launch: it waits for this grid to finish
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  volatile int* abort_flag = &bars->abort;
+  PagedWalk<C::TK> w(p, plan.run);
+
+  if (warp == C::WARPS) {
+    // ------------------------------------------------------------ TMA producer
+    const int box_shift = min(p.page_shift, 6), boxes = C::TK >> box_shift;
+    const int n_op = boxes * 2 * (D / 64);  // copies per tile: boxes x (K, V) x 64-column blocks
+    PagedPages pages;
+    int g = 0;
+    bool ok = true;
+    while (ok && w.next()) {
+      if (lane == 0 && p.kv_len[w.it.b] > w.it.kv) atomicExch(&g_spa_status, kStatusInval);
+      const int hk = w.it.hg / p.kv_div;
+      for (int t = w.t0; t < w.t1; ++t, ++g) {
+        const int s = g % C::NS;
+        const int box_i = lane % boxes, op = lane / boxes;  // op: (K or V) x column block
+        const int64_t box0 = (int64_t)t * boxes;
+        const int id0 = pages.get(p, w.it, box0, box_shift, boxes, box_i, t == w.t0);
+        ok = __all_sync(0xffffffffu, bar_wait(&bars->empty[s], ((g / C::NS) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->full[s], C::STAGE_BYTES);
+        __syncwarp();
+        if (lane < n_op) {
+          const bool is_v = op >= D / 64;
+          const int cb = op % (D / 64);
+          const int64_t j = (box0 + box_i) << box_shift;
+          ptx::tma_load_3d(smem + s * C::STAGE_BYTES + (is_v ? C::KV_BYTES : 0) + cb * (C::TK * 128) +
+                               (box_i << box_shift) * 128,
+                           is_v ? &tm_v : &tm_k, &bars->full[s], cb * 64, (int)(j & ((1 << p.page_shift) - 1)),
+                           id0 < 0 ? -1 : id0 * p.Hk + hk);
+        }
+        __syncwarp();
+      }
+    }
+    // every copy issued has landed before the CTA ends
+    if (lane == 0)
+      for (int s = 0; s < C::NS; ++s) {
+        const int used = (g + C::NS - 1 - s) / C::NS;  // times this warp armed stage s
+        if (used > 0) bar_drain(&bars->full[s], (used - 1) & 1);
+      }
+    return;
+  }
+
+  // ------------------------------------------------------------ four warps, 16 keys of a tile each
+  const uint32_t s_base = ptx::smem_u32(smem);
+  float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
+  float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
+  float* s_l = s_m + C::WARPS * C::ROWS;
+  const int quad = lane / 4, qc = lane % 4;
+  int g = 0, job = -1, followers = 0;
+  // A warp whose wait runs out of time computes no further tile, but walks on
+  // through the pieces, so that the named barriers keep their four warps.
+  bool ok = true;
+  while (w.next()) {
+    const PagedItem& it = w.it;
+    const int rows = it.tokens * p.group;
+    // this lane's two rows: their queries as A operands, their permitted keys
+    uint32_t qf[D / 16][4];
+    int64_t a_lo[2], a_hi[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = quad + 8 * x;
+      const bool live = r < rows;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + paged_row(p, it, live ? r : 0) * D);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        qf[kk][x] = live ? src[kk * 8 + qc] : 0u;
+        qf[kk][x + 2] = live ? src[kk * 8 + 4 + qc] : 0u;
+      }
+      const int64_t pos = it.pos0 + r / p.group;
+      a_lo[x] = live ? max64(0, pos - p.hi[it.hg] + 1) : 0;
+      a_hi[x] = live ? min64(pos - p.lo[it.hg], it.kv - 1) : -1;
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+
+    for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+      const int s = g % C::NS;
+      ok = __all_sync(0xffffffffu, bar_wait(&bars->full[s], (g / C::NS) & 1, abort_flag));
+      if (!ok) break;
+      const int64_t j0 = (int64_t)t * C::TK + warp * 16;
+      if (j0 <= it.jhi && j0 + 15 >= it.jlo) {
+        const uint32_t k_base = s_base + s * C::STAGE_BYTES, v_base = k_base + C::KV_BYTES;
+        // S = Q K^T: two 8-key column tiles
+        float sc[2][4] = {};
+        {
+          const int mat = lane / 8, key = warp * 16 + lane % 8 + (mat >= 2 ? 8 : 0);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int chunk = kk * 2 + (mat & 1);
+            uint32_t kf[4];
+            ldmatrix_x4(kf, k_base + (chunk / 8) * (C::TK * 128) + ptx::sw128_offset(key, chunk % 8));
+            mma_16816<E>(sc[0], qf[kk], kf[0], kf[1]);
+            mma_16816<E>(sc[1], qf[kk], kf[2], kf[3]);
+          }
+        }
+        // masked scores become -inf; base-2 units
+        uint32_t pa[4];
+        float alpha[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int c_lo = (int)max64(min64(a_lo[x] - j0, 16), 0), c_hi = (int)max64(min64(a_hi[x] - j0, 15), -1);
+          float v[4], mx = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = (e / 2) * 8 + 2 * qc + (e & 1);
+            v[e] = c >= c_lo && c <= c_hi ? sc[e / 2][2 * x + (e & 1)] * p.scale_log2 : -INFINITY;
+            mx = ptx::fmax_nan(mx, v[e]);
+          }
+          mx = ptx::fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = ptx::fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = ptx::fmax_nan(m[x], mx);
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          alpha[x] = ptx::exp2_approx(m[x] - ref);
+          m[x] = m_new;
+          float pe[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pe[e] = ptx::exp2_approx(v[e] - ref);
+          l[x] = fmaf(l[x], alpha[x], (pe[0] + pe[1]) + (pe[2] + pe[3]));
+          pa[x] = E::pack(pe[0], pe[1]);
+          pa[x + 2] = E::pack(pe[2], pe[3]);
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            acc[n][0] *= alpha[0];
+            acc[n][1] *= alpha[0];
+            acc[n][2] *= alpha[1];
+            acc[n][3] *= alpha[1];
+          }
+        }
+        // O += P V.  Values of keys that no row attends to are cleared: what
+        // stands there may be no number, and 0 times that is none either.
+        {
+          uint32_t keep[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int64_t j = j0 + 8 * x + 2 * qc;
+            keep[x] = (j >= it.jlo && j <= it.jhi ? 0xffffu : 0u) |
+                      (j + 1 >= it.jlo && j + 1 <= it.jhi ? 0xffff0000u : 0u);
+          }
+          const int mat = lane / 8, key = warp * 16 + lane % 8 + (mat & 1) * 8;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            const int chunk = n * 2 + mat / 2;
+            uint32_t vf[4];
+            ldmatrix_x4_trans(vf, v_base + (chunk / 8) * (C::TK * 128) + ptx::sw128_offset(key, chunk % 8));
+            mma_16816<E>(acc[2 * n], pa, vf[0] & keep[0], vf[1] & keep[1]);
+            mma_16816<E>(acc[2 * n + 1], pa, vf[2] & keep[0], vf[3] & keep[1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bars->empty[s]);
+    }
+
+    // ---------------------------------------------------------- the four warps' results meet
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+      if (qc == 0) {
+        s_m[warp * C::ROWS + quad + 8 * x] = m[x];
+        s_l[warp * C::ROWS + quad + 8 * x] = l[x];
+      }
+    }
+    ptx::named_bar_sync(1, C::WARPS * 32);
+    float f[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float mx = s_m[quad + 8 * x];
+#pragma unroll
+      for (int y = 1; y < C::WARPS; ++y) mx = ptx::fmax_nan(mx, s_m[y * C::ROWS + quad + 8 * x]);
+      f[x] = m[x] == -INFINITY ? 0.f : ptx::exp2_approx(m[x] - mx);
+    }
+    float* slot = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D);
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+      const int x = r0 / 8;  // these four rows are the lanes' first or second
+      if (quad - r0 % 8 >= 0 && quad - r0 % 8 < 4) {
+        float* dst = s_red + (warp * 4 + quad - r0 % 8) * D + 2 * qc;
+        const float fx = x ? f[1] : f[0];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(dst + n * 8) =
+              make_float2((x ? acc[n][2] : acc[n][0]) * fx, (x ? acc[n][3] : acc[n][1]) * fx);
+      }
+      ptx::named_bar_sync(1, C::WARPS * 32);
+      const int r = r0 + warp;  // one row per warp now, D / 32 columns per lane
+      if (r < rows) {
+        constexpr int CW = D / 32;
+        float mx = s_m[r], sum = 0.f, out[CW] = {};
+#pragma unroll
+        for (int y = 1; y < C::WARPS; ++y) mx = ptx::fmax_nan(mx, s_m[y * C::ROWS + r]);
+#pragma unroll
+        for (int y = 0; y < C::WARPS; ++y) {
+          const float my = s_m[y * C::ROWS + r];
+          sum += my == -INFINITY ? 0.f : s_l[y * C::ROWS + r] * ptx::exp2_approx(my - mx);
+#pragma unroll
+          for (int e = 0; e < CW; ++e) out[e] += s_red[(y * 4 + warp) * D + lane * CW + e];
+        }
+        if (w.whole) {
+          const int64_t row = paged_row(p, it, r);
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (CW / 2);
+#pragma unroll
+          for (int e = 0; e < CW / 2; ++e) dst[e] = E::pack(out[2 * e] * inv, out[2 * e + 1] * inv);
+          if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+        } else {
+#pragma unroll
+          for (int e = 0; e < CW; ++e) slot[r * D + lane * CW + e] = out[e];
+          if (lane == 0) {
+            slot[C::ROWS * D + r] = mx;
+            slot[C::ROWS * D + C::ROWS + r] = sum;
+          }
+        }
+      }
+      ptx::named_bar_sync(1, C::WARPS * 32);
+    }
+    if (!w.whole && w.begins) {
+      job = w.item;
+      followers = (int)((it.cost - w.len + plan.run.run - 1) / plan.run.run);
+    }
+  }
+  if (threadIdx.x == 0) paged_describe(p, ok ? job : -1, followers);
+}
+
+// ------------------------------------------------------------------ merge
+// CTA x joins the partials of the item that CTA x of the main kernel began
+// and left unfinished: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over
+// its pieces, in their order.  One warp per row; grid y shares the rows.
+template <class E, int D, int ROWS, int TK>
+__global__ void __launch_bounds__(128) spa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int item = p.desc[2 * c], n = p.desc[2 * c + 1] + 1;
+  // (a CTA of the main kernel that could not run has described nothing)
+  if (item < 0 || item >= p.B * p.ng * p.nblk || n < 1 || c + n > (int)gridDim.x) return;
+  constexpr int CW = D / 32;
+  constexpr int64_t SLOT = paged_slot_floats(ROWS, D);
+  const PagedItem it = paged_item_at<TK>(p, item);
+  const int rows = it.tokens * p.group;
+  // piece 0 lies in slot 2c + 1, piece i in slot 2 (c + i)
+  const float* base = p.part + 2 * (int64_t)c * SLOT;
+  for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
+    float mx = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+      mx = ptx::fmax_nan(mx, base[(i ? 2 * i : 1) * SLOT + ROWS * D + r]);
+#pragma unroll
+    for (int k = 16; k > 0; k /= 2) mx = ptx::fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    float sum = 0.f, out[CW] = {};
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      float f = 0.f, li = 0.f;
+      if (i < n) {
+        const float* ml = base + (i ? 2 * i : 1) * SLOT + ROWS * D + r;
+        f = ml[0] == -INFINITY ? 0.f : ptx::exp2_approx(ml[0] - mx);
+        li = ml[ROWS] * f;
+      }
+#pragma unroll 4
+      for (int k = 0; k < min(32, n - i0); ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        sum += __shfl_sync(0xffffffffu, li, k);
+        const float* src = base + (i0 + k ? 2 * (i0 + k) : 1) * SLOT + r * D + lane * CW;
+        float v[CW];
+        if constexpr (CW == 4) {
+          const float4 u = *reinterpret_cast<const float4*>(src);
+          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+        } else {
+          const float2 u = *reinterpret_cast<const float2*>(src);
+          v[0] = u.x; v[1] = u.y;
+        }
+        // a piece in which the row attends to nothing counts for nothing
+#pragma unroll
+        for (int e = 0; e < CW; ++e) out[e] = fk == 0.f ? out[e] : fmaf(fk, v[e], out[e]);
+      }
+    }
+    const int64_t row = paged_row(p, it, r);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (CW / 2);
+#pragma unroll
+    for (int e = 0; e < CW / 2; ++e) dst[e] = E::pack(out[2 * e] * inv, out[2 * e + 1] * inv);
+    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace spa

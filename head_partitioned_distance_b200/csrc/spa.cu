@@ -19,6 +19,7 @@
 #include "decode.cuh"
 #include "fwd.cuh"
 #include "norm_rope.cuh"
+#include "paged.cuh"
 #include "sched.cuh"
 #include "union.cuh"
 
@@ -777,6 +778,79 @@ int log2_of(int page) {
   return s;
 }
 
+// ------------------------------------------------------------ paged attention
+// [pages][Hk][page][d] cache viewed as 3-D (d, page, pages * Hk): boxes of 64
+// columns x `rows` positions of one page and head; a page outside fills with
+// zeros.
+int make_page_map(CUtensorMap* m, const void* ptr, int64_t pages, int Hk, int page, int d, int rows, int dtype) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SPA_ERR_CUDA;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)pages * (cuuint64_t)Hk};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)page * (cuuint64_t)d * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, dtype == SPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPA_OK : SPA_ERR_CUDA;
+}
+
+// CTAs of the kernel for few rows: two on each of a B200's 148 SMs.  Each has
+// two partial slots in the workspace, after the merge's descriptions.
+constexpr int kPagedShortCtas = 296;
+constexpr size_t kPagedDescBytes = 4096;
+static_assert(kPagedShortCtas * 2 * sizeof(int32_t) <= kPagedDescBytes, "descriptions");
+constexpr int kPagedMaxSplit = 32;
+
+struct PagedCall {
+  const void* k_pages;
+  const void* v_pages;
+  int page, d, dtype;
+};
+
+template <class E, int D>
+int paged_short_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
+  using C = spa::PagedShortCfg<D>;
+  static std::atomic<uint64_t> prepared;
+  CUtensorMap mk, mv;
+  int st;
+  const int rows = std::min(c.page, C::TK);
+  if ((st = make_page_map(&mk, c.k_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)) ||
+      (st = make_page_map(&mv, c.v_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)))
+    return st;
+  auto* kernel = spa::spa_paged_short_kernel<E, D>;
+  if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
+  kernel<<<kPagedShortCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mk, mv, p);
+  if ((st = launch_status())) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPagedShortCtas, 1, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, spa::spa_paged_merge_kernel<E, D, C::ROWS, C::TK>, p) != cudaSuccess)
+    return SPA_ERR_CUDA;
+  return launch_status();
+}
+
+// Groups the query heads into work items of `group` heads (a divisor of the
+// heads per key/value head) with blocks of `tokens` rows.
+int paged_items(spa::PagedParams& p, const AttnParams& bands, int group, int tokens) {
+  p.group = group;
+  p.ng = p.Hq / group;
+  p.kv_div = p.ng / p.Hk;
+  p.blk_tokens = tokens;
+  p.nblk = (p.max_q + tokens - 1) / tokens;
+  for (int g = 0; g < p.ng; ++g) {
+    p.lo[g] = bands.lo[g * group];
+    p.hi[g] = bands.hi[g * group];
+  }
+  return (int64_t)p.B * p.ng * p.nblk > 2147483647LL ? SPA_ERR_UNSUPPORTED : SPA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1352,6 +1426,65 @@ int spa_paged_append(const void* q, const void* k, const void* v, const float* w
   p.heads_per_group = norm_rope_heads(T, Hq + 2 * Hk, d, sms);
   p.eps = eps;
   return norm_rope_dispatch<PagedAppend>(dtype, d, interleaved != 0, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t spa_paged_attn_workspace_bytes(int max_q, int d) {
+  if (max_q < 1 || (d != 64 && d != 128)) return 0;
+  return kPagedDescBytes + (size_t)kPagedShortCtas * 2 * spa::paged_slot_floats(16, d) * sizeof(float);
+}
+
+int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                   const int32_t* cu_q, const int32_t* kv_len, void* o, float* lse, void* workspace, int B, int T,
+                   int max_q, int Hq, int Hk, int64_t pages, int page, int width, int64_t N, int d, float scale,
+                   const int32_t* lo, const int32_t* hi, int dtype, void* stream) {
+  if (B < 1 || T < 0 || max_q < 1 || Hq < 1 || Hk < 1 || Hq % Hk || pages < 1 || width < 1 || N < 1 ||
+      N > 2147483647LL || check_dtype(dtype) || !std::isfinite(scale) || !(scale > 0.f))
+    return SPA_ERR_INVAL;
+  if (B > 65535 || Hq > spa::kMaxHeads || (d != 64 && d != 128) || !valid_page(page) ||
+      pages > 2147483647LL / Hk)
+    return SPA_ERR_UNSUPPORTED;
+  int st;
+  AttnParams bands{};
+  if ((st = fill_bands(bands, Hq, N, lo, hi))) return st;
+  if (T == 0) return SPA_OK;
+  if (!q || !k_pages || !v_pages || !page_table || !cu_q || !kv_len || !o || !lse || !workspace) return SPA_ERR_INVAL;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(o, 32) || !aligned(lse, 4) ||
+      !aligned(page_table, 4) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(workspace, 256))
+    return SPA_ERR_UNSUPPORTED;
+  spa::PagedParams p{};
+  p.cu_q = cu_q;
+  p.kv_len = kv_len;
+  p.page_table = page_table;
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.desc = static_cast<int32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedDescBytes);
+  p.pages = pages;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hk = Hk;
+  p.max_q = std::min(max_q, T);
+  p.width = width;
+  p.page_shift = log2_of(page);
+  p.scale_log2 = scale * spa::kLog2e;
+  // query heads that share a key/value head and have one band
+  const int per_kv = Hq / Hk;
+  bool same = true;
+  for (int h = 0; h < Hq; ++h)
+    same = same && bands.lo[h] == bands.lo[h - h % per_kv] && bands.hi[h] == bands.hi[h - h % per_kv];
+  int group = 1;
+  for (int g = 1; same && g <= std::min(per_kv, 16); ++g)
+    if (per_kv % g == 0 && (int64_t)g * p.max_q <= 16) group = g;
+  p.min_run = 2;
+  p.max_split = kPagedMaxSplit;
+  if ((st = paged_items(p, bands, group, 16 / group))) return st;
+  const PagedCall c{k_pages, v_pages, page, d, dtype};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dtype == SPA_BF16)
+    return d == 64 ? paged_short_launch<spa::Bf16, 64>(c, p, s) : paged_short_launch<spa::Bf16, 128>(c, p, s);
+  return d == 64 ? paged_short_launch<spa::Fp16, 64>(c, p, s) : paged_short_launch<spa::Fp16, 128>(c, p, s);
 }
 
 }  // extern "C"

@@ -78,6 +78,9 @@ EXPORTS = {
                                            _int, _f32, _int, _vp], _int),
     "spa_paged_append": ([_vp] * 12 + [_int, _int, _int, _int, _int, _i64, _int, _int, _int, _i64, _i64p, _i64p, _i64p,
                                        _int, _f32, _int, _vp], _int),
+    "spa_paged_attn_workspace_bytes": ([_int, _int], ctypes.c_size_t),
+    "spa_paged_attn": ([_vp] * 9 + [_int, _int, _int, _int, _int, _i64, _int, _int, _i64, _int, _f32, _i32p, _i32p,
+                                    _int, _vp], _int),
 }
 for _name, (_args, _res) in EXPORTS.items():
     _fn = getattr(_lib, _name)
@@ -889,3 +892,51 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q_weight, 
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
     return spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, out, k_pages, v_pages, eps,
                             interleaved)
+
+
+def spa_paged_attn_workspace_bytes(max_q: int, d: int) -> int:
+    return int(_lib.spa_paged_attn_workspace_bytes(max_q, d))
+
+
+def spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, o, lse, workspace, N: int, scale: float,
+                   lo=None, hi=None, stream=None):
+    """Attention of the new tokens' q [T, Hq, d] over the paged cache: writes
+    o [T, Hq, d] and lse [T, Hq] fp32 (spa.h).  Bands: lo / hi per query head,
+    or the Balanced Distance Partitioning ones of length N."""
+    if q.dim() != 3 or k_pages.dim() != 4:
+        raise ValueError("q is [T, Hq, d], k_pages and v_pages are [pages, Hk, page, d]")
+    T, Hq, d = q.shape
+    Hk = k_pages.shape[1]
+    dt, dev = _dtype_code(q, "q"), q.device
+    _need_on(q, (T, Hq, d), q.dtype, dev, "q")
+    _need_on(o, (T, Hq, d), q.dtype, dev, "o")
+    _need_on(lse, (T, Hq), torch.float32, dev, "lse")
+    B, pages, page, width = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, q.dtype, dev)
+    if workspace.device != dev or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < spa_paged_attn_workspace_bytes(max_q, d):
+        raise ValueError("workspace: contiguous CUDA tensor of spa_paged_attn_workspace_bytes(max_q, d) bytes")
+    if (lo is not None and len(lo) != Hq) or (hi is not None and len(hi) != Hq):
+        raise ValueError(f"lo and hi: {Hq} entries, one for each query head")
+    lo_a = None if lo is None else _i32(lo)
+    hi_a = None if hi is None else _i32(hi)
+    with _on(dev):
+        _check(_lib.spa_paged_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                   cu_q.data_ptr(), kv_len.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                   workspace.data_ptr(), B, T, max_q, Hq, Hk, pages, page, width, N, d, scale, lo_a,
+                                   hi_a, dt, _stream_on(dev, stream)), "spa_paged_attn")
+    return o, lse
+
+
+def paged_attention(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, scale=None, lo=None, hi=None, N=None,
+                    out=None, lse=None):
+    """Attention of the new tokens (one or many per sequence) over the paged
+    cache; allocates o / lse (unless given as out, lse; rows behind the last
+    sequence are not written) and the workspace and runs spa_paged_attn.  N,
+    the length the bands belong to, defaults to what the page table can hold."""
+    d = q.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    N = page_table.shape[-1] * k_pages.shape[2] if N is None else N
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
+    ws = torch.empty(max(spa_paged_attn_workspace_bytes(max_q, d) // 4, 1), dtype=torch.float32, device=q.device)
+    return spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, out, lse, ws, N, scale, lo, hi)

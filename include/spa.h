@@ -545,6 +545,46 @@ SPA_API int spa_paged_append(const void* q, const void* k, const void* v, const 
                              const int64_t* q_strides, const int64_t* k_strides, const int64_t* v_strides,
                              int interleaved, float eps, int dtype, void* stream);
 
+/*
+ * Attention of the new tokens over the paged cache (their own keys and values
+ * already in it).  Token row r of sequence b, at position p, attends with query
+ * head h to
+ *   S = { j : 0 <= j < kv_len[b], lo_h <= p - j < hi_h },
+ * through key/value head h / (Hq / Hk); o and lse as in spa_attn_fwd.  A row
+ * with empty S gets o = 0 and lse = -inf.  With the bands of the training
+ * length N this equals row p of spa_attn_fwd on the whole sequence.
+ *   q:         DEVICE [T][Hq][d]
+ *   o:         DEVICE [T][Hq][d];  lse: DEVICE fp32 [T][Hq], natural log
+ *   max_q:     no sequence has more new tokens; rows past that many of one
+ *              sequence are not written
+ *   N, lo, hi: length of the bands: HOST arrays of Hq entries with
+ *              0 <= lo < hi <= N, or both NULL for the Balanced Distance
+ *              Partitioning bands of length N (requires Hq <= N).  Keys with
+ *              equal bands on all query heads of a key/value head are read
+ *              once for all of them.
+ *   workspace: DEVICE buffer of spa_paged_attn_workspace_bytes(max_q, d)
+ *              bytes, 256-byte aligned, caller-owned, overwritten; two calls
+ *              that may overlap need two
+ * Pages that hold no key some row attends to are not read, and their entries
+ * in the page table may be anything; so may what stands in keys and values
+ * that no row attends to.  Keys and values of a sequence that some of its new
+ * rows attend to and others do not must be finite.  A page number outside
+ * [0, pages) that is needed, or a kv_len beyond the page table, counts as keys
+ * of zeros there or as no keys, and spa_device_status reports SPA_ERR_INVAL.
+ * Lengths are read on the device only: a captured call follows them.  Two
+ * launches; results are the same from call to call.  T = 0 launches nothing.
+ * SPA_ERR_INVAL for null pointers, sizes < 1, Hq not a multiple of Hk, bad
+ * bands, a scale that is not finite and > 0 or an unknown dtype;
+ * SPA_ERR_UNSUPPORTED for d not in {64, 128}, Hq > 256, B > 65535, a page size
+ * outside the rule above, pages * Hk > 2^31 - 1, too many rows for a 32-bit
+ * work list, or misaligned buffers (32 bytes for o, 16 for q, k_pages,
+ * v_pages, 4 for the integers and lse).
+ */
+SPA_API size_t spa_paged_attn_workspace_bytes(int max_q, int d);
+SPA_API int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                           const int32_t* cu_q, const int32_t* kv_len, void* o, float* lse, void* workspace, int B,
+                           int T, int max_q, int Hq, int Hk, int64_t pages, int page, int width, int64_t N, int d,
+                           float scale, const int32_t* lo, const int32_t* hi, int dtype, void* stream);
 #ifdef __cplusplus
 }
 #endif

@@ -110,3 +110,36 @@ def test_binding_refuses_cpu_tensors():
         spa.paged_append(x[0], x[0], x[0], x, x, None, None, None, w, w, t)
     with pytest.raises(ValueError, match="B, H, N, d"):
         spa.qk_norm_rope(x[0], x[0], w, w, t)
+
+
+def test_paged_attention_refuses():
+    def att(p=None, B=2, T=5, max_q=3, Hq=4, Hk=2, pages=10, page=16, width=3, N=48, d=64, scale=0.1, lo=None, hi=None,
+            dtype=0):
+        p = list(p or [P] * 9)
+        a = None if lo is None else (ctypes.c_int32 * len(lo))(*lo)
+        b = None if hi is None else (ctypes.c_int32 * len(hi))(*hi)
+        return spa._lib.spa_paged_attn(*p, B, T, max_q, Hq, Hk, pages, page, width, N, d, scale, a, b, dtype, None)
+
+    inval = [dict(B=0), dict(T=-1), dict(max_q=0), dict(Hq=0), dict(Hk=0), dict(Hq=5), dict(pages=0), dict(width=0),
+             dict(N=0), dict(N=1 << 31), dict(N=3), dict(scale=0.0), dict(scale=float("nan")), dict(dtype=2),
+             dict(lo=[0] * 4), dict(lo=[0] * 4, hi=[0] * 4), dict(lo=[-1] * 4, hi=[9] * 4),
+             dict(lo=[0] * 4, hi=[49] * 4)]
+    for kw in inval:
+        assert att(**kw) == spa.SPA_ERR_INVAL, kw
+    unsupported = [dict(B=65536), dict(Hq=258, N=300), dict(d=96), dict(page=8), dict(page=24), dict(page=512),
+                   dict(pages=1 << 30)]
+    for kw in unsupported:
+        assert att(**kw) == spa.SPA_ERR_UNSUPPORTED, kw
+    assert att([None] * 9, T=0) == spa.SPA_OK
+    for i in range(9):
+        p = [P] * 9
+        p[i] = None
+        assert att(p) == spa.SPA_ERR_INVAL
+        p[i] = _fake((1 << 20) + 2)
+        assert att(p) == spa.SPA_ERR_UNSUPPORTED
+    p = [P] * 9
+    p[6] = _fake((1 << 20) + 16)  # o is written in 32-byte stores
+    assert att(p) == spa.SPA_ERR_UNSUPPORTED
+    p[6], p[8] = P, _fake((1 << 20) + 128)
+    assert att(p) == spa.SPA_ERR_UNSUPPORTED
+    assert spa.spa_paged_attn_workspace_bytes(0, 64) == spa.spa_paged_attn_workspace_bytes(1, 96) == 0
