@@ -45,4 +45,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
 }
 
+// 32 fp32 values times `mul` -> 32 16-bit values at `dst` (64 bytes, 32-byte
+// aligned).
+template <class E>
+__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&g)[32], float mul) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) pk[e] = E::pack(__uint_as_float(g[2 * e]) * mul, __uint_as_float(g[2 * e + 1]) * mul);
+  ptx::st_global_v8(dst, pk);
+  ptx::st_global_v8(dst + 16, pk + 8);
+}
+
 }  // namespace spa

@@ -20,6 +20,7 @@
 #include "fwd.cuh"
 #include "norm_rope.cuh"
 #include "paged.cuh"
+#include "paged_long.cuh"
 #include "sched.cuh"
 #include "union.cuh"
 
@@ -797,16 +798,34 @@ int make_page_map(CUtensorMap* m, const void* ptr, int64_t pages, int Hk, int pa
 
 // CTAs of the kernel for few rows: two on each of a B200's 148 SMs.  Each has
 // two partial slots in the workspace, after the merge's descriptions.
-constexpr int kPagedShortCtas = 296;
+// The kernel for many rows has one CTA per SM.
+constexpr int kPagedShortCtas = 296, kPagedLongCtas = 148;
 constexpr size_t kPagedDescBytes = 4096;
 static_assert(kPagedShortCtas * 2 * sizeof(int32_t) <= kPagedDescBytes, "descriptions");
-constexpr int kPagedMaxSplit = 32;
+constexpr int kPagedShortSplit = 32, kPagedLongSplit = 16;
 
 struct PagedCall {
   const void* k_pages;
   const void* v_pages;
   int page, d, dtype;
 };
+
+// Joins the divided items of the main kernel launched before it, as its
+// programmatic dependent: `ctas` x `shares` blocks, the rows of an item shared.
+template <class E, int D, int ROWS, int TK>
+int paged_merge_launch(const spa::PagedParams& p, int ctas, int shares, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)shares, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, spa::spa_paged_merge_kernel<E, D, ROWS, TK>, p) != cudaSuccess) return SPA_ERR_CUDA;
+  return launch_status();
+}
 
 template <class E, int D>
 int paged_short_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
@@ -822,18 +841,47 @@ int paged_short_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) 
   if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
   kernel<<<kPagedShortCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mk, mv, p);
   if ((st = launch_status())) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPagedShortCtas, 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, spa::spa_paged_merge_kernel<E, D, C::ROWS, C::TK>, p) != cudaSuccess)
-    return SPA_ERR_CUDA;
-  return launch_status();
+  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedShortCtas, 1, s);
+}
+
+// q [T][Hq][d] viewed as 4-D (d, heads of a group, groups, T): a box holds 64
+// columns of one group's heads of 128 / group tokens, the heads fastest.
+int make_paged_q_map(CUtensorMap* m, const spa::PagedParams& p, int d, int dtype) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SPA_ERR_CUDA;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.group, (cuuint64_t)p.ng, (cuuint64_t)p.T};
+  cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)p.group * d * 2, (cuuint64_t)p.Hq * d * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)p.group, 1, (cuuint32_t)(128 / p.group)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, dtype == SPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                   const_cast<uint16_t*>(p.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPA_OK : SPA_ERR_CUDA;
+}
+
+template <class E, int D>
+int paged_long_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
+  using C = spa::PagedLongCfg<D>;
+  static std::atomic<uint64_t> prepared[2];
+  static std::atomic<int> regs_ok[2];
+  // the softmax warpgroups take turns when the bands are wide on average (the
+  // forward's rule, kFwdTurnMinWidth)
+  int64_t width_sum = 0;
+  for (int g = 0; g < p.ng; ++g) width_sum += (int64_t)p.hi[g] - p.lo[g];
+  const bool turn = width_sum >= kFwdTurnMinWidth * (int64_t)p.ng;
+  CUtensorMap mq, mk, mv;
+  int st;
+  const int rows = std::min(c.page, C::TK);
+  if ((st = make_paged_q_map(&mq, p, D, c.dtype)) ||
+      (st = make_page_map(&mk, c.k_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)) ||
+      (st = make_page_map(&mv, c.v_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)))
+    return st;
+  auto* kernel = turn ? spa::spa_paged_long_kernel<E, D, true> : spa::spa_paged_long_kernel<E, D, false>;
+  if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared[turn]))) return st;
+  if ((st = check_regs(kernel, (int)C::LAUNCH_REGS, regs_ok[turn]))) return st;
+  kernel<<<kPagedLongCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mq, mk, mv, p);
+  if ((st = launch_status())) return st;
+  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedLongCtas, 8, s);
 }
 
 // Groups the query heads into work items of `group` heads (a divisor of the
@@ -1430,7 +1478,9 @@ int spa_paged_append(const void* q, const void* k, const void* v, const float* w
 
 size_t spa_paged_attn_workspace_bytes(int max_q, int d) {
   if (max_q < 1 || (d != 64 && d != 128)) return 0;
-  return kPagedDescBytes + (size_t)kPagedShortCtas * 2 * spa::paged_slot_floats(16, d) * sizeof(float);
+  const int64_t few = 2 * kPagedShortCtas * spa::paged_slot_floats(16, d);
+  const int64_t many = 2 * kPagedLongCtas * spa::paged_slot_floats(256, d);
+  return kPagedDescBytes + (size_t)std::max(few, many) * sizeof(float);
 }
 
 int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -1474,17 +1524,25 @@ int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, cons
   bool same = true;
   for (int h = 0; h < Hq; ++h)
     same = same && bands.lo[h] == bands.lo[h - h % per_kv] && bands.hi[h] == bands.hi[h - h % per_kv];
-  int group = 1;
-  for (int g = 1; same && g <= std::min(per_kv, 16); ++g)
-    if (per_kv % g == 0 && (int64_t)g * p.max_q <= 16) group = g;
-  p.min_run = 2;
-  p.max_split = kPagedMaxSplit;
-  if ((st = paged_items(p, bands, group, 16 / group))) return st;
   const PagedCall c{k_pages, v_pages, page, d, dtype};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((int64_t)p.max_q * (same ? per_kv : 1) <= 16) {
+    const int group = same ? per_kv : 1;
+    p.min_run = 2;
+    p.max_split = kPagedShortSplit;
+    if ((st = paged_items(p, bands, group, 16 / group))) return st;
+    if (dtype == SPA_BF16)
+      return d == 64 ? paged_short_launch<spa::Bf16, 64>(c, p, s) : paged_short_launch<spa::Bf16, 128>(c, p, s);
+    return d == 64 ? paged_short_launch<spa::Fp16, 64>(c, p, s) : paged_short_launch<spa::Fp16, 128>(c, p, s);
+  }
+  int group = 1;
+  while (same && group < 128 && per_kv % (2 * group) == 0) group *= 2;
+  p.min_run = 2;
+  p.max_split = kPagedLongSplit;
+  if ((st = paged_items(p, bands, group, 256 / group))) return st;
   if (dtype == SPA_BF16)
-    return d == 64 ? paged_short_launch<spa::Bf16, 64>(c, p, s) : paged_short_launch<spa::Bf16, 128>(c, p, s);
-  return d == 64 ? paged_short_launch<spa::Fp16, 64>(c, p, s) : paged_short_launch<spa::Fp16, 128>(c, p, s);
+    return d == 64 ? paged_long_launch<spa::Bf16, 64>(c, p, s) : paged_long_launch<spa::Bf16, 128>(c, p, s);
+  return d == 64 ? paged_long_launch<spa::Fp16, 64>(c, p, s) : paged_long_launch<spa::Fp16, 128>(c, p, s);
 }
 
 }  // extern "C"
