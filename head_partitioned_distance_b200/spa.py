@@ -9,7 +9,6 @@ library reports an error.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -649,39 +648,50 @@ def spa_attn_union_add_grads(dq, dk, dv, dq2, dk2, dv2, stream=None):
 DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # spa_dtype_t
 
 
-def _on(device):
-    """Makes `device` current for a launch (the launch goes to the current device)."""
+def _launch(device, where: str, fn, *args):
+    """Calls a C entry point with `device` current (the launch goes there)."""
     if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != SPA_OK:
+        raise SpaError(status, where)
 
 
 def _stream_on(device, stream):
-    return _vp((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    """The stream's handle, or that of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _dtype_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in DTYPES or not t.is_cuda:
+    code = DTYPES.get(t.dtype)
+    if code is None or not t.is_cuda:
         raise ValueError(f"{name}: expected CUDA bfloat16 or float16 tensor, got {t.dtype} on {t.device}")
-    return DTYPES[t.dtype]
+    return code
 
 
 def _need_on(t, shape, dtype, device, name):
     """A contiguous tensor of this shape and type on `device`."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _vector_rows(t) -> bool:
     """Rows (the last dimension) contiguous and every row 16-byte aligned."""
-    return t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and \
-        all(s % 8 == 0 or n == 1 for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    *outer, last = t.stride()
+    if last != 1 or t.data_ptr() % 16:
+        return False
+    for n, s in zip(t.shape, outer):
+        if s % 8 and n != 1:
+            return False
+    return True
 
 
 def _need_rows(t, shape, dtype, device, name):
     """A tensor of this shape and type on `device`, its rows readable in 16-byte vectors."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not _vector_rows(t):
@@ -689,9 +699,12 @@ def _need_rows(t, shape, dtype, device, name):
                          f"multiples of 8, got strides {t.stride()}")
 
 
+_Strides2, _Strides3 = _i64 * 2, _i64 * 3
+
+
 def _strides(t):
-    n = t.dim() - 1
-    return (ctypes.c_int64 * n)(*t.stride()[:n])
+    s = t.stride()
+    return _Strides3(*s[:3]) if len(s) == 4 else _Strides2(*s[:2])
 
 
 def _rope_args(table, positions, B, N, device):
@@ -723,9 +736,8 @@ def spa_rope_table(table, base: float, stream=None):
     if table.dim() != 3 or table.shape[2] != 2 or not table.is_cuda:
         raise ValueError(f"table: expected CUDA tensor [length, rot / 2, 2], got {tuple(table.shape)} on {table.device}")
     _need_on(table, table.shape, torch.float32, table.device, "table")
-    with _on(table.device):
-        _check(_lib.spa_rope_table(table.data_ptr(), table.shape[0], 2 * table.shape[1], base,
-                                   _stream_on(table.device, stream)), "spa_rope_table")
+    _launch(table.device, "spa_rope_table", _lib.spa_rope_table, table.data_ptr(), table.shape[0], 2 * table.shape[1],
+            base, _stream_on(table.device, stream))
     return table
 
 
@@ -748,11 +760,9 @@ def spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, q_out, k_out, position
     _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
     _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
     rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
-    with _on(dev):
-        _check(_lib.spa_qk_norm_rope_fwd(q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(),
-                                         table.data_ptr(), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d,
-                                         rot, table.shape[0], pos_stride, _strides(q), _strides(k), int(interleaved),
-                                         eps, dt, _stream_on(dev, stream)), "spa_qk_norm_rope_fwd")
+    _launch(dev, "spa_qk_norm_rope_fwd", _lib.spa_qk_norm_rope_fwd, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
+            k_weight.data_ptr(), table.data_ptr(), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d, rot,
+            table.shape[0], pos_stride, _strides(q), _strides(k), int(interleaved), eps, dt, _stream_on(dev, stream))
     return q_out, k_out
 
 
@@ -777,40 +787,38 @@ def spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk
             workspace.numel() * workspace.element_size() < spa_qk_norm_rope_bwd_workspace_bytes(d):
         raise ValueError("workspace: contiguous CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes")
     rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
-    with _on(dev):
-        _check(_lib.spa_qk_norm_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                                         q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), pos,
-                                         dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(),
-                                         workspace.data_ptr(), B, Hq, Hk, N, d, rot, table.shape[0], pos_stride,
-                                         _strides(q), _strides(k), _strides(dq), _strides(dk), int(interleaved), eps,
-                                         dt, _stream_on(dev, stream)), "spa_qk_norm_rope_bwd")
+    _launch(dev, "spa_qk_norm_rope_bwd", _lib.spa_qk_norm_rope_bwd, dq_out.data_ptr(), dk_out.data_ptr(),
+            q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), pos,
+            dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), B, Hq, Hk,
+            N, d, rot, table.shape[0], pos_stride, _strides(q), _strides(k), _strides(dq), _strides(dk),
+            int(interleaved), eps, dt, _stream_on(dev, stream))
     return dq, dk, dq_weight, dk_weight
 
 
 def qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6,
                          interleaved: bool = False):
     """Allocate q_out / k_out (contiguous) and run spa_qk_norm_rope_fwd."""
-    qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ko = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+    ko = torch.empty_like(k, memory_format=torch.contiguous_format)
     return spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, qo, ko, positions, eps, interleaved)
 
 
 def _grad_like(x):
     """An empty gradient of x [B, H, N, d], dense and in x's order of heads and rows."""
     B, H, N, d = x.shape
-    if x.stride(1) < x.stride(2):
-        return torch.empty((B, N, H, d), dtype=x.dtype, device=x.device).transpose(1, 2)
-    return torch.empty((B, H, N, d), dtype=x.dtype, device=x.device)
+    _, sh, sn, _ = x.stride()
+    strides = (N * H * d, d, H * d, 1) if sh < sn else (H * N * d, N * d, d, 1)
+    return torch.empty_strided(x.shape, strides, dtype=x.dtype, device=x.device)
 
 
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6,
                           interleaved: bool = False):
     """Allocate dq / dk / dq_weight / dk_weight / workspace and run spa_qk_norm_rope_bwd."""
     d = q.shape[-1]
-    dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
-    ws = torch.empty(max(spa_qk_norm_rope_bwd_workspace_bytes(d) // 4, 1), dtype=torch.float32, device=q.device)
-    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, _grad_like(q), _grad_like(k), dw[0],
-                                dw[1], ws, positions, eps, interleaved)
+    dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
+    ws = q_weight.new_empty(spa_qk_norm_rope_bwd_workspace_bytes(d) // 4)
+    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, _grad_like(q), _grad_like(k), dwq,
+                                dwk, ws, positions, eps, interleaved)
 
 
 class QKNormRopeFunction(torch.autograd.Function):
@@ -874,13 +882,11 @@ def spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_tabl
     _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
     B, pages, page, width = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, q.dtype, dev)
     rot, _, _ = _rope_args(table, None, 1, 0, dev)
-    with _on(dev):
-        _check(_lib.spa_paged_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_weight.data_ptr(),
-                                     k_weight.data_ptr(), table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
-                                     page_table.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                                     B, T, Hq, Hk, d, pages, page, width, rot, table.shape[0], _strides(q),
-                                     _strides(k), _strides(v), int(interleaved), eps, dt, _stream_on(dev, stream)),
-               "spa_paged_append")
+    _launch(dev, "spa_paged_append", _lib.spa_paged_append, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
+            page_table.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, T, Hq, Hk, d, pages,
+            page, width, rot, table.shape[0], _strides(q), _strides(k), _strides(v), int(interleaved), eps, dt,
+            _stream_on(dev, stream))
     return q_out
 
 
@@ -889,7 +895,7 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q_weight, 
     """Norm and rotate the new tokens' queries and keys, store keys and values in
     the paged cache, return the queries (allocated unless given as out; rows
     behind the last sequence are not written)."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
     return spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, out, k_pages, v_pages, eps,
                             interleaved)
 
@@ -919,11 +925,10 @@ def spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, o,
         raise ValueError(f"lo and hi: {Hq} entries, one for each query head")
     lo_a = None if lo is None else _i32(lo)
     hi_a = None if hi is None else _i32(hi)
-    with _on(dev):
-        _check(_lib.spa_paged_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                                   cu_q.data_ptr(), kv_len.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                   workspace.data_ptr(), B, T, max_q, Hq, Hk, pages, page, width, N, d, scale, lo_a,
-                                   hi_a, dt, _stream_on(dev, stream)), "spa_paged_attn")
+    _launch(dev, "spa_paged_attn", _lib.spa_paged_attn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr(), B, T, max_q, Hq, Hk, pages, page, width, N, d, scale, lo_a, hi_a, dt,
+            _stream_on(dev, stream))
     return o, lse
 
 
@@ -936,7 +941,7 @@ def paged_attention(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, s
     d = q.shape[-1]
     scale = d ** -0.5 if scale is None else scale
     N = page_table.shape[-1] * k_pages.shape[2] if N is None else N
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if lse is None else lse
-    ws = torch.empty(max(spa_paged_attn_workspace_bytes(max_q, d) // 4, 1), dtype=torch.float32, device=q.device)
+    ws = lse.new_empty(spa_paged_attn_workspace_bytes(max_q, d) // 4)
     return spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q, out, lse, ws, N, scale, lo, hi)
