@@ -701,15 +701,16 @@ int norm_rope_heads(int64_t tokens, int heads, int d, int sms) {
   int64_t split = (groups + tokens - 1) / tokens;  // lane groups wanted per token
   split = split < 1 ? 1 : split;
   const int64_t per = (heads + split - 1) / split;
-  const int64_t lo = spa::kNrUnroll, hi = 4 * spa::kNrUnroll;
-  return (int)(per < lo ? lo : per > hi ? hi : per);
+  return (int)std::max<int64_t>(per, spa::kNrUnroll);
 }
+
+int head_chunks(int heads, int per) { return (heads + per - 1) / per; }
 
 template <class E, int D, bool NB>
 int norm_rope_fwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
   constexpr int TOK = spa::kNrThreads / (D / 8);
-  const int heads = p.Hq + p.Hk;
-  const dim3 grid((unsigned)((p.tokens + TOK - 1) / TOK), (unsigned)((heads + p.heads_per_group - 1) / p.heads_per_group));
+  const dim3 grid((unsigned)((p.tokens + TOK - 1) / TOK),
+                  (unsigned)(head_chunks(p.Hq, p.heads_per_group) + head_chunks(p.Hk, p.heads_per_group)));
   spa::spa_qk_norm_rope_fwd_kernel<E, D, NB><<<grid, spa::kNrThreads, 0, s>>>(p);
   return launch_status();
 }
@@ -717,15 +718,17 @@ int norm_rope_fwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
 template <class E, int D, bool NB>
 int norm_rope_bwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
   constexpr int TOK = spa::kNrThreads / (D / 8);
-  const int64_t chunks = (p.Hq + p.Hk + p.heads_per_group - 1) / p.heads_per_group;
-  const int64_t units = (p.tokens + TOK - 1) / TOK * chunks;
-  const int blocks = (int)(units < spa::kNrMaxBlocks ? units : spa::kNrMaxBlocks);
+  const int64_t tiles = (p.tokens + TOK - 1) / TOK;
+  const int64_t uq = tiles * head_chunks(p.Hq, p.heads_per_group), uk = tiles * head_chunks(p.Hk, p.heads_per_group);
+  // the blocks are shared between query and key heads in proportion
+  p.q_blocks = (int)std::min<int64_t>(uq, std::max<int64_t>(1, (int64_t)spa::kNrMaxBlocks * p.Hq / (p.Hq + p.Hk)));
+  const int blocks = p.q_blocks + (int)std::min<int64_t>(uk, std::max<int64_t>(1, spa::kNrMaxBlocks - p.q_blocks));
   spa::spa_qk_norm_rope_bwd_kernel<E, D, NB><<<blocks, spa::kNrThreads, 0, s>>>(p);
   int st = launch_status();
   if (st) return st;
   // the sum of the partials starts its launch while the last blocks finish
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32, 1, 1);
+  cfg.gridDim = dim3(D / 32, 2, 1);
   cfg.blockDim = dim3(1024, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -733,7 +736,8 @@ int norm_rope_bwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, spa::spa_qk_norm_rope_dw_kernel<D>, (const float*)p.part, blocks, p.dwq, p.dwk) !=
+  if (cudaLaunchKernelEx(&cfg, spa::spa_qk_norm_rope_dw_kernel<D>, (const float*)p.part, p.q_blocks, blocks, p.dwq,
+                         p.dwk) !=
       cudaSuccess)
     return SPA_ERR_CUDA;
   return launch_status();
@@ -742,8 +746,8 @@ int norm_rope_bwd_launch(spa::NormRopeParams& p, cudaStream_t s) {
 template <class E, int D, bool NB>
 int paged_append_launch(spa::AppendParams& p, cudaStream_t s) {
   constexpr int TOK = spa::kNrThreads / (D / 8);
-  const int heads = p.Hq + 2 * p.Hk;
-  const dim3 grid((unsigned)((p.T + TOK - 1) / TOK), (unsigned)((heads + p.heads_per_group - 1) / p.heads_per_group));
+  const dim3 grid((unsigned)((p.T + TOK - 1) / TOK),
+                  (unsigned)(head_chunks(p.Hq, p.heads_per_group) + 2 * head_chunks(p.Hk, p.heads_per_group)));
   spa::spa_paged_append_kernel<E, D, NB><<<grid, spa::kNrThreads, 0, s>>>(p);
   return launch_status();
 }
@@ -1370,7 +1374,7 @@ int spa_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, const fl
 
 size_t spa_qk_norm_rope_bwd_workspace_bytes(int d) {
   if (d != 64 && d != 128) return 0;
-  return (size_t)spa::kNrMaxBlocks * 2 * (size_t)d * sizeof(float);
+  return (size_t)(spa::kNrMaxBlocks + 1) * (size_t)d * sizeof(float);
 }
 
 int spa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* wq,
