@@ -54,12 +54,15 @@ struct PagedItem {
   int b, hg;
   int row0;      // first token row
   int tokens;    // token rows; 0: nothing to do
-  int64_t pos0;  // position of the first
-  int64_t jlo, jhi;  // keys that some row attends to (jhi < jlo: none)
-  int64_t kv;    // keys the sequence has (and the page table can name)
+  int pos0;      // position of the first
+  int jlo, jhi;  // keys that some row attends to (jhi < jlo: none)
+  int kv;        // keys the sequence has (and the page table can name)
   int t0;        // first key tile
   int cost;      // steps; an item without keys takes one
 };
+
+// Positions and lengths are 32-bit; sums of them with band limits need more.
+__device__ __forceinline__ int clamp_i32(int64_t v) { return (int)max64(min64(v, 2147483647LL), -2147483648LL); }
 
 template <int TK>
 __device__ __forceinline__ PagedItem paged_item(const PagedParams& p, int b, int hg, int blk) {
@@ -72,13 +75,14 @@ __device__ __forceinline__ PagedItem paged_item(const PagedParams& p, int b, int
   const int first = blk * p.blk_tokens;
   it.row0 = c0 + first;
   it.tokens = max(0, min(p.blk_tokens, n - first));
-  it.pos0 = (int64_t)len - n_all + first;
-  it.kv = min64(max(len, 0), (int64_t)p.width << p.page_shift);
-  it.jlo = max64(0, it.pos0 - p.hi[hg] + 1);
-  it.jhi = min64(it.pos0 + it.tokens - 1 - p.lo[hg], it.kv - 1);
+  const int64_t pos0 = (int64_t)len - n_all + first;
+  it.pos0 = clamp_i32(pos0);
+  it.kv = (int)min64(max(len, 0), (int64_t)p.width << p.page_shift);
+  it.jlo = (int)max64(0, pos0 - p.hi[hg] + 1);
+  it.jhi = clamp_i32(min64(pos0 + it.tokens - 1 - p.lo[hg], it.kv - 1));
   const bool any = it.tokens > 0 && it.jhi >= it.jlo;
-  it.t0 = any ? (int)(it.jlo / TK) : 0;
-  it.cost = it.tokens == 0 ? 0 : any ? (int)(it.jhi / TK) - it.t0 + 1 : 1;
+  it.t0 = any ? it.jlo / TK : 0;
+  it.cost = it.tokens == 0 ? 0 : any ? it.jhi / TK - it.t0 + 1 : 1;
   return it;
 }
 
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(160, 2)
     const int rows = it.tokens * p.group;
     // this lane's two rows: their queries as A operands, their permitted keys
     uint32_t qf[D / 16][4];
-    int64_t a_lo[2], a_hi[2];
+    int a_lo[2], a_hi[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int r = quad + 8 * x;
@@ -391,9 +395,9 @@ __global__ void __launch_bounds__(160, 2)
         qf[kk][x] = live ? src[kk * 8 + qc] : 0u;
         qf[kk][x + 2] = live ? src[kk * 8 + 4 + qc] : 0u;
       }
-      const int64_t pos = it.pos0 + r / p.group;
-      a_lo[x] = live ? max64(0, pos - p.hi[it.hg] + 1) : 0;
-      a_hi[x] = live ? min64(pos - p.lo[it.hg], it.kv - 1) : -1;
+      const int64_t pos = (int64_t)it.pos0 + r / p.group;
+      a_lo[x] = live ? (int)max64(0, pos - p.hi[it.hg] + 1) : 0;
+      a_hi[x] = live ? clamp_i32(min64(pos - p.lo[it.hg], it.kv - 1)) : -1;
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float acc[D / 8][4];
@@ -406,8 +410,8 @@ __global__ void __launch_bounds__(160, 2)
       const int s = g % C::NS;
       ok = __all_sync(0xffffffffu, bar_wait(&bars->full[s], (g / C::NS) & 1, abort_flag));
       if (!ok) break;
-      const int64_t j0 = (int64_t)t * C::TK + warp * 16;
-      if (j0 <= it.jhi && j0 + 15 >= it.jlo) {
+      const int j0 = t * C::TK + warp * 16;  // at most 2^31 - 16: the last key stands below 2^31
+      if (j0 <= it.jhi && j0 >= it.jlo - 15) {
         const uint32_t k_base = s_base + s * C::STAGE_BYTES, v_base = k_base + C::KV_BYTES;
         // S = Q K^T: two 8-key column tiles
         float sc[2][4] = {};
@@ -427,7 +431,7 @@ __global__ void __launch_bounds__(160, 2)
         float alpha[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int c_lo = (int)max64(min64(a_lo[x] - j0, 16), 0), c_hi = (int)max64(min64(a_hi[x] - j0, 15), -1);
+          const int c_lo = a_lo[x] - j0, c_hi = a_hi[x] - j0;
           float v[4], mx = -INFINITY;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -463,9 +467,9 @@ __global__ void __launch_bounds__(160, 2)
           uint32_t keep[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int64_t j = j0 + 8 * x + 2 * qc;
+            const int j = j0 + 8 * x + 2 * qc;
             keep[x] = (j >= it.jlo && j <= it.jhi ? 0xffffu : 0u) |
-                      (j + 1 >= it.jlo && j + 1 <= it.jhi ? 0xffff0000u : 0u);
+                      (j + 1 >= it.jlo && j < it.jhi ? 0xffff0000u : 0u);
           }
           const int mat = lane / 8, key = warp * 16 + lane % 8 + (mat & 1) * 8;
 #pragma unroll

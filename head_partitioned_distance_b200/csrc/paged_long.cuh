@@ -22,61 +22,93 @@
 // cycles of the 16 special-function lanes and 512 of the tensor core).
 #pragma once
 
-#include "fwd.cuh"
 #include "paged.cuh"
 
 namespace spa {
 
+// K and V have rings of their own: a K stage is free as soon as both tiles'
+// S are done, a V stage after both tiles' O products, so that each is asked
+// for about two steps before it is used.  (With one ring for both, released
+// after the O products, a step of keys from DRAM took 3.5 us instead of XX.)
 template <int D>
-struct PagedLongCfg : FwdCfg<D> {
+struct PagedLongCfg {
   static constexpr int ROWS = 256, TK = 128;
-  using F = FwdCfg<D>;
-  static constexpr uint32_t OFF_PLAN = F::OFF_BAR + 256;
+  static constexpr int BQ = 128, BK = TK, DB = D / 64;
+  static constexpr int NK = D == 128 ? 3 : 4, NV = D == 128 ? 2 : 4;
+  static constexpr uint32_t Q_BYTES = BQ * D * 2, KV_BYTES = BK * D * 2;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
+  static constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_V + NV * KV_BYTES;
+  static constexpr uint32_t OFF_PLAN = OFF_BAR + 384;
   static constexpr uint32_t USED = OFF_PLAN + 512;
+  // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
   static constexpr uint32_t SMEM_BYTES = USED + 1024 > 116u * 1024 ? USED + 1024 : 116u * 1024;
   static_assert(SMEM_BYTES <= kMaxSmemPerBlock, "shared memory");
+  static constexpr int NTHREADS = 384;
+  // register split (fwd.cuh): 168 per thread at launch
+  static constexpr uint32_t LAUNCH_REGS = 168, SOFTMAX_REGS = 200, CONTROL_REGS = 104;
+  static_assert(2 * SOFTMAX_REGS + CONTROL_REGS <= 3 * LAUNCH_REGS, "register split over budget");
+  static constexpr uint32_t TMEM_COLS = 512;
+  // tile t: S (and P over its first half) at t*256, O at t*256 + 128
+  __host__ __device__ static constexpr uint32_t tm_s(int t) { return (uint32_t)(t * 256); }
+  __host__ __device__ static constexpr uint32_t tm_o(int t) { return (uint32_t)t * 256u + 128u; }
 };
 
 struct PagedLongBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[2], v_full[2], kv_empty[2];
-  uint64_t v_fixed[2];  // the helper warp has cleared the rows outside the key range
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-  uint64_t turn[2];
+  uint64_t k_full[4], k_empty[4];
+  uint64_t v_full[4], v_empty[4];
+  uint64_t v_fixed[4];   // the helper warp has cleared the rows outside the key range
+  uint64_t s_full[2];
+  uint64_t p_full[2][2];  // [tile][half of the keys]
+  uint64_t o_done[2], o_free[2];
+  uint64_t turn[2];       // turn[t]: softmax warpgroup t may form its exponentials
+  uint64_t done[2][2];    // done[t][piece % 2]: warpgroup t is past its last turn of the piece
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(PagedLongBars) <= 256, "barrier space");
+static_assert(sizeof(PagedLongBars) <= 384, "barrier space");
 
-// One piece of an item as the two Q tiles see it.
-struct PagedTiles {
-  int rows[2];     // rows of the tile that exist
-  int64_t pos[2];  // position of the tile's first and last token
-  int64_t last[2];
-  int a[2], b[2];  // its key tiles within the piece
-  bool act[2];
-  int u0, u1;
+// A stage of a ring of N and the parity of its current phase.
+template <int N>
+struct RingSlot {
+  int s = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      par ^= 1;
+    }
+  }
+};
+
+// One Q tile's part in a piece: its existing rows and its key tiles.
+struct PagedTile {
+  int rows;
+  int a, b;  // b < a: no key of this piece is attended to
+  int first_pos, last_pos;
+  __device__ __forceinline__ bool has(int kt) const { return kt >= a && kt <= b; }
+  __device__ __forceinline__ bool active() const { return b >= a; }
 };
 
 template <int TK>
-__device__ __forceinline__ PagedTiles paged_tiles(const PagedParams& p, const PagedWalk<TK>& w) {
-  PagedTiles U;
+__device__ __forceinline__ PagedTile paged_tile(const PagedParams& p, const PagedWalk<TK>& w, int t) {
   const PagedItem& it = w.it;
   const int per = 128 / p.group;  // tokens per Q tile
-  U.u0 = w.t0;
-  U.u1 = w.t1 - 1;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int tok = max(0, min(per, it.tokens - t * per));
-    U.rows[t] = tok * p.group;
-    U.pos[t] = it.pos0 + t * per;
-    U.last[t] = U.pos[t] + tok - 1;
-    const int64_t jlo = max64(0, U.pos[t] - p.hi[it.hg] + 1), jhi = min64(U.last[t] - p.lo[it.hg], it.kv - 1);
-    U.act[t] = tok > 0 && jhi >= jlo;
-    U.a[t] = U.act[t] ? max((int)(jlo / TK), w.t0) : 0;
-    U.b[t] = U.act[t] ? min((int)(jhi / TK), w.t1 - 1) : -1;
-    U.act[t] = U.act[t] && U.a[t] <= U.b[t];
+  const int tok = max(0, min(per, it.tokens - t * per));
+  PagedTile U;
+  U.rows = tok * p.group;
+  U.first_pos = it.pos0 + t * per;
+  U.last_pos = U.first_pos + tok - 1;
+  const int64_t jlo = max64(0, (int64_t)U.first_pos - p.hi[it.hg] + 1);
+  const int64_t jhi = min64((int64_t)U.last_pos - p.lo[it.hg], it.kv - 1);
+  U.a = 1;
+  U.b = 0;
+  if (tok > 0 && jhi >= jlo) {
+    U.a = max((int)(jlo / TK), w.t0);
+    U.b = min((int)(jhi / TK), w.t1 - 1);
   }
   return U;
 }
@@ -84,10 +116,34 @@ __device__ __forceinline__ PagedTiles paged_tiles(const PagedParams& p, const Pa
 // The item's key range cuts tile `t`: some of its rows are not to be used.
 template <int TK>
 __device__ __forceinline__ bool paged_cut(const PagedItem& it, int t) {
-  return (int64_t)t * TK < it.jlo || (int64_t)t * TK + TK - 1 > it.jhi;
+  return t * TK < it.jlo || t * TK > it.jhi - (TK - 1);
 }
 
-template <class E, int D, bool TURN>
+// Scores of 32 columns that lie outside [lo, hi] (counted from the first of
+// them) become -inf.
+__device__ __forceinline__ void paged_mask32(uint32_t (&s)[32], int lo, int hi) {
+  const uint32_t from = lo > 31 ? 0u : 0xffffffffu << max(lo, 0);
+  const uint32_t to = hi < 0 ? 0u : 0xffffffffu >> (31 - min(hi, 31));
+  const uint32_t keep = from & to;
+#pragma unroll
+  for (int e = 0; e < 32; ++e) s[e] = (keep >> e) & 1 ? s[e] : 0xff800000u;
+}
+
+// p = 2^(s c2 + mneg) of 32 scores as 16-bit pairs; adds them up in fp32.
+template <class E>
+__device__ __forceinline__ void paged_exp32(const uint32_t (&s)[32], float2 c2v, float2 mnv, float2& sa, float2& sb,
+                                            uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2v, mnv);
+    const float2 y = make_float2(ptx::exp2_approx(x.x), ptx::exp2_approx(x.y));
+    if (e & 1) sb = __fadd2_rn(sb, y);
+    else sa = __fadd2_rn(sa, y);
+    pk[e] = E::pack(y.x, y.y);
+  }
+}
+
+template <class E, int D>
 __global__ void __launch_bounds__(384, 1)
     spa_paged_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedParams p) {
@@ -106,16 +162,24 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars->q_full[i], 1);
       ptx::mbar_init(&bars->q_empty[i], 1);
-      ptx::mbar_init(&bars->k_full[i], 1);
-      ptx::mbar_init(&bars->v_full[i], 1);
-      ptx::mbar_init(&bars->v_fixed[i], 1);
-      ptx::mbar_init(&bars->kv_empty[i], 3);  // one release per MMA issuer, one of the helper's
       ptx::mbar_init(&bars->s_full[i], 1);
-      ptx::mbar_init(&bars->p_full[i], 128);
+      ptx::mbar_init(&bars->p_full[i][0], 128);
+      ptx::mbar_init(&bars->p_full[i][1], 128);
       ptx::mbar_init(&bars->o_done[i], 1);
       ptx::mbar_init(&bars->o_free[i], 128);
       ptx::mbar_init(&bars->turn[i], 128);
+      ptx::mbar_init(&bars->done[i][0], 128);
+      ptx::mbar_init(&bars->done[i][1], 128);
       ptx::mbar_init(&bars->drain[i], 1);
+    }
+    for (int i = 0; i < C::NK; ++i) {
+      ptx::mbar_init(&bars->k_full[i], 1);
+      ptx::mbar_init(&bars->k_empty[i], 2);  // one release per MMA issuer
+    }
+    for (int i = 0; i < C::NV; ++i) {
+      ptx::mbar_init(&bars->v_full[i], 1);
+      ptx::mbar_init(&bars->v_fixed[i], 1);
+      ptx::mbar_init(&bars->v_empty[i], 3);  // one release per MMA issuer, one of the helper's
     }
     bars->abort = 0;
     ptx::fence_mbar_init();
@@ -143,178 +207,201 @@ __global__ void __launch_bounds__(384, 1)
       // ---------------------------------------------------------- helper: clears unused V rows
       // It follows every tile, cut or not, and releases the stage like an MMA
       // issuer, so that the waits on v_full keep step with its phases.
-      int g = 0;
+      RingSlot<C::NV> v;
       bool ok = true;
       while (ok && w.next()) {
         const PagedItem& it = w.it;
-        for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-          const int s = g % C::NS;
-          ok = __all_sync(0xffffffffu, bar_wait(&bars->v_full[s], (g / C::NS) & 1, abort_flag));
+        for (int t = w.t0; t < w.t1; ++t, v.next()) {
+          ok = __all_sync(0xffffffffu, bar_wait(&bars->v_full[v.s], v.par, abort_flag));
           if (!ok) break;
-          if (!paged_cut<C::TK>(it, t)) {
-            if (lane == 0) ptx::mbar_arrive(&bars->kv_empty[s]);
-            continue;
-          }
-          const int64_t j0 = (int64_t)t * C::TK;
-          const int first = (int)min64(max64(it.jlo - j0, 0), C::TK);    // rows [0, first) and
-          const int end = (int)min64(max64(it.jhi + 1 - j0, 0), C::TK);  // [end, TK) are not used
-          const int n = first + (C::TK - end);
-          for (int e = lane; e < n * 8; e += 32) {
-            const int r = e / 8 < first ? e / 8 : end + e / 8 - first;
+          const bool cut = paged_cut<C::TK>(it, t);
+          if (cut) {
+            const int j0 = t * C::TK;
+            const int first = min(max(it.jlo - j0, 0), C::TK);    // rows [0, first) and
+            const int end = min(max(it.jhi + 1 - j0, 0), C::TK);  // [end, TK) are not used
+            const int n = first + (C::TK - end);
+            for (int e = lane; e < n * 8; e += 32) {
+              const int r = e / 8 < first ? e / 8 : end + e / 8 - first;
 #pragma unroll
-            for (int c = 0; c < C::DB; ++c)
-              ptx::st_shared_v4(sV + s * C::KV_BYTES + c * (C::BK * 128) + r * 128 + (e % 8) * 16, 0u, 0u, 0u, 0u);
+              for (int c = 0; c < C::DB; ++c)
+                ptx::st_shared_v4(sV + v.s * C::KV_BYTES + c * (C::BK * 128) + r * 128 + (e % 8) * 16, 0u, 0u, 0u, 0u);
+            }
+            ptx::fence_proxy_async_smem();
           }
-          ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            ptx::mbar_arrive(&bars->v_fixed[s]);
-            ptx::mbar_arrive(&bars->kv_empty[s]);
+            if (cut) ptx::mbar_arrive(&bars->v_fixed[v.s]);
+            ptx::mbar_arrive(&bars->v_empty[v.s]);
           }
         }
       }
     } else if (warp == 8) {
       // ---------------------------------------------------------- TMA producer
+      // Asks for K of a tile one step ahead of V of the tile before.
       const int box_shift = min(p.page_shift, 7), boxes = C::TK >> box_shift;
+      const int box_i = lane % boxes, cb = lane / boxes;  // box, 64-column block
       PagedPages pages;
-      int nq[2] = {0, 0};
-      int g = 0;
+      RingSlot<C::NK> k;
+      RingSlot<C::NV> v;
+      int nq[2] = {0, 0}, nk = 0, nv = 0;
       bool ok = true;
       while (ok && w.next()) {
         const PagedItem& it = w.it;
-        const PagedTiles U = paged_tiles(p, w);
         const int hk = it.hg / p.kv_div;
         if (lane == 0 && p.kv_len[it.b] > it.kv) atomicExch(&g_spa_status, kStatusInval);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || !U.act[t]) continue;
-          ok = __all_sync(0xffffffffu, bar_wait(&bars->q_empty[t], (nq[t] & 1) ^ 1, abort_flag));
-          if (!ok) continue;
-          ++nq[t];
-          if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(&bars->q_full[t], C::Q_BYTES);
-            for (int c = 0; c < C::DB; ++c)
-              ptx::tma_load_4d(smem + C::OFF_Q + t * C::Q_BYTES + c * (C::BQ * 128), &tm_q, &bars->q_full[t], c * 64,
-                               0, it.hg, it.row0 + t * (128 / p.group));
-          }
-        }
-        for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-          const int s = g % C::NS;
-          const int box_i = lane % boxes, cb = lane / boxes;  // box, 64-column block
-          const int64_t box0 = (int64_t)t * boxes;
-          const int id = pages.get(p, it, box0, box_shift, boxes, box_i, t == w.t0);
-          ok = __all_sync(0xffffffffu, bar_wait(&bars->kv_empty[s], ((g / C::NS) & 1) ^ 1, abort_flag));
-          if (!ok) break;
-          if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(&bars->k_full[s], C::KV_BYTES);
-            ptx::mbar_arrive_expect_tx(&bars->v_full[s], C::KV_BYTES);
-          }
+        // one 128-key tile of K or V into a stage, a box per page and 64 columns
+        auto fetch = [&](const CUtensorMap* map, uint32_t at, uint64_t* bar, int t, int id) {
+          if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::KV_BYTES);
           __syncwarp();
           if (cb < C::DB) {
-            const int64_t j = (box0 + box_i) << box_shift;
-            const int c1 = (int)(j & ((1 << p.page_shift) - 1)), c2 = id < 0 ? -1 : id * p.Hk + hk;
-            const uint32_t at = s * C::KV_BYTES + cb * (C::BK * 128) + (box_i << box_shift) * 128;
-            ptx::tma_load_3d(smem + C::OFF_K + at, &tm_k, &bars->k_full[s], cb * 64, c1, c2);
-            ptx::tma_load_3d(smem + C::OFF_V + at, &tm_v, &bars->v_full[s], cb * 64, c1, c2);
+            const int j = (t * boxes + box_i) << box_shift;
+            ptx::tma_load_3d(smem + at + cb * (C::BK * 128) + (box_i << box_shift) * 128, map, bar, cb * 64,
+                             j & ((1 << p.page_shift) - 1), id < 0 ? -1 : id * p.Hk + hk);
           }
           __syncwarp();
+        };
+        int id_v = -1;
+        for (int t = w.t0; t <= w.t1; ++t) {
+          int id = -1;
+          if (t < w.t1) {
+            id = pages.get(p, it, (int64_t)t * boxes, box_shift, boxes, box_i, t == w.t0);
+            ok = __all_sync(0xffffffffu, bar_wait(&bars->k_empty[k.s], k.par ^ 1, abort_flag));
+            if (!ok) break;
+            fetch(&tm_k, C::OFF_K + k.s * C::KV_BYTES, &bars->k_full[k.s], t, id);
+            k.next();
+            ++nk;
+            if (t == w.t0) {
+              // Q after the first K: its buffers are free only when the piece
+              // before has done its last S
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                if (!ok || !paged_tile(p, w, x).active()) continue;
+                ok = __all_sync(0xffffffffu, bar_wait(&bars->q_empty[x], (nq[x] & 1) ^ 1, abort_flag));
+                if (!ok) continue;
+                ++nq[x];
+                if (lane == 0) {
+                  ptx::mbar_arrive_expect_tx(&bars->q_full[x], C::Q_BYTES);
+                  for (int c = 0; c < C::DB; ++c)
+                    ptx::tma_load_4d(smem + C::OFF_Q + x * C::Q_BYTES + c * (C::BQ * 128), &tm_q, &bars->q_full[x],
+                                     c * 64, 0, it.hg, it.row0 + x * (128 / p.group));
+                }
+              }
+              if (!ok) break;
+            }
+          }
+          if (t > w.t0) {
+            ok = __all_sync(0xffffffffu, bar_wait(&bars->v_empty[v.s], v.par ^ 1, abort_flag));
+            if (!ok) break;
+            fetch(&tm_v, C::OFF_V + v.s * C::KV_BYTES, &bars->v_full[v.s], t - 1, id_v);
+            v.next();
+            ++nv;
+          }
+          id_v = id;
         }
       }
       // Exit path: every load this warp issued has landed before the CTA ends.
       if (lane == 0) {
         for (int t = 0; t < 2; ++t)
           if (nq[t] > 0) bar_drain(&bars->q_full[t], (nq[t] - 1) & 1);
-        for (int s = 0; s < C::NS; ++s) {
-          const int used = (g + C::NS - 1 - s) / C::NS;
-          if (used > 0) {
-            bar_drain(&bars->k_full[s], (used - 1) & 1);
-            bar_drain(&bars->v_full[s], (used - 1) & 1);
-          }
+        for (int s = 0; s < C::NK; ++s) {
+          const int used = (nk + C::NK - 1 - s) / C::NK;
+          if (used > 0) bar_drain(&bars->k_full[s], (used - 1) & 1);
+        }
+        for (int s = 0; s < C::NV; ++s) {
+          const int used = (nv + C::NV - 1 - s) / C::NV;
+          if (used > 0) bar_drain(&bars->v_full[s], (used - 1) & 1);
         }
       }
     } else {
       // ---------------------------------------------------------- MMA issuers
-      // warp 9 issues every MMA of Q tile 0, warp 10 those of Q tile 1 (fwd.cuh)
+      // warp 9 issues every MMA of Q tile 0, warp 10 those of Q tile 1; both
+      // walk the piece's whole key range, so they agree on the rings
       const int t = warp - 9;
       if (lane == 0) {
         constexpr uint32_t idesc_s = ptx::idesc_16_f32(E::kMmaFormat, 128, C::BK, false, false);
         constexpr uint32_t idesc_o = ptx::idesc_16_f32(E::kMmaFormat, 128, D, false, true);
         const uint64_t dq = ptx::sdesc_sw128(sQ + t * C::Q_BYTES, 0, 1024);
-        const uint64_t dk0 = ptx::sdesc_sw128(sK, 0, 1024), dk1 = ptx::sdesc_sw128(sK + C::KV_BYTES, 0, 1024);
-        const uint64_t dv0 = ptx::sdesc_sw128(sV, C::BK * 128, 1024);
-        const uint64_t dv1 = ptx::sdesc_sw128(sV + C::KV_BYTES, C::BK * 128, 1024);
-        const uint32_t tS = tmem + C::tm_s(t), tO = tmem + C::tm_o(t);
+        const uint64_t dk = ptx::sdesc_sw128(sK, 0, 1024), dv = ptx::sdesc_sw128(sV, C::BK * 128, 1024);
+        const uint32_t tO = tmem + C::tm_o(t);
+        const uint32_t tS = tmem + C::tm_s(t);
         uint64_t* s_full = &bars->s_full[t];
-        uint64_t* p_full = &bars->p_full[t];
-        int cq = 0, cp = 0, co = 0, g = 0;
+        RingSlot<C::NK> k;
+        RingSlot<C::NV> v;
+        int cq = 0, co = 0;
+        uint32_t cp = 0;     // parity of the next P
         uint32_t fixed = 0;  // bit s: parity of the next v_fixed[s] phase
         bool ok = true;
-        auto issue_s = [&](int slot) {
-          const uint64_t db = slot ? dk1 : dk0;
+        auto wait_k = [&]() { ok = ok && bar_wait(&bars->k_full[k.s], k.par, abort_flag); };
+        auto wait_v = [&](int kt) {
+          ok = ok && bar_wait(&bars->v_full[v.s], v.par, abort_flag);
+          if (ok && paged_cut<C::TK>(w.it, kt)) {
+            ok = bar_wait(&bars->v_fixed[v.s], (fixed >> v.s) & 1, abort_flag);
+            fixed ^= 1u << v.s;
+          }
+        };
+        auto issue_s = [&]() {
+          const uint64_t db = ptx::sdesc_advance(dk, k.s * C::KV_BYTES);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             ptx::mma_bf16(tS, ptx::sdesc_advance(dq, (kk / 4) * (C::BQ * 128) + (kk % 4) * 32),
                           ptx::sdesc_advance(db, (kk / 4) * (C::BK * 128) + (kk % 4) * 32), idesc_s, kk > 0);
           ptx::mma_commit(s_full);
+          ptx::mma_commit(&bars->k_empty[k.s]);
+          k.next();
         };
-        auto issue_pv = [&](int slot, bool first) {
-          const uint64_t db = slot ? dv1 : dv0;
-          ptx::mma_bf16_ts(tO, tS, db, idesc_o, !first);
-#pragma unroll
-          for (int kk = 1; kk < C::BK / 16; ++kk)
-            ptx::mma_bf16_ts(tO, tS + kk * 8, ptx::sdesc_advance(db, kk * (16 * 128)), idesc_o, 1);
+        auto skip = [&](int kt) {  // a key tile that this Q tile does not use
+          wait_k();
+          if (ok) ptx::mbar_arrive(&bars->k_empty[k.s]);
+          k.next();
+          wait_v(kt);
+          if (ok) ptx::mbar_arrive(&bars->v_empty[v.s]);
+          v.next();
         };
         while (ok && w.next()) {
-          const PagedTiles U = paged_tiles(p, w);
-          if (U.u1 < U.u0) continue;
-          const bool act_t = t ? U.act[1] : U.act[0];
-          const int a_t = t ? U.a[1] : U.a[0];
-          const int b_t = t ? U.b[1] : U.b[0];
-          auto act = [&](int it) { return act_t && it >= a_t && it <= b_t; };
-          const int g0 = g;
-          auto slot = [&](int it) { return (g0 + it - U.u0) % C::NS; };
-          auto ring_par = [&](int it) { return (uint32_t)(((g0 + it - U.u0) / C::NS) & 1); };
-          if (act_t) ok = bar_wait(&bars->q_full[t], (cq++) & 1, abort_flag);
-          bool first = true;
-          ok = ok && bar_wait(&bars->k_full[slot(U.u0)], ring_par(U.u0), abort_flag);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          if (act(U.u0)) {
-            issue_s(slot(U.u0));
-            if (U.u0 == b_t) ptx::mma_commit(&bars->q_empty[t]);
-          }
-          for (int it = U.u0; ok && it <= U.u1; ++it) {
-            const int s = slot(it);
-            ok = bar_wait(&bars->v_full[s], ring_par(it), abort_flag);
-            if (ok && paged_cut<C::TK>(w.it, it)) {
-              ok = bar_wait(&bars->v_fixed[s], (fixed >> s) & 1, abort_flag);
-              fixed ^= 1u << s;
-            }
+          if (w.t1 <= w.t0) continue;
+          const PagedTile U = paged_tile(p, w, t);
+          const int a = U.active() ? U.a : w.t1, b = U.active() ? U.b : w.t1 - 1;
+          for (int kt = w.t0; ok && kt < a; ++kt) skip(kt);
+          if (U.active()) {
+            ok = ok && bar_wait(&bars->q_full[t], (cq++) & 1, abort_flag);
+            wait_k();
             if (!ok) break;
-            if (act(it)) {
-              // O_t += P_t V, then release the stage (this tile's reads of it are issued)
-              ok = bar_wait(p_full, (cp++) & 1, abort_flag);
-              if (ok && first) ok = bar_wait(&bars->o_free[t], ((co++) & 1) ^ 1, abort_flag);
+            ptx::tc_fence_after();
+            issue_s();
+            if (a == b) ptx::mma_commit(&bars->q_empty[t]);
+            for (int kt = a; kt <= b; ++kt) {
+              // Everything else that the next products need is waited for before
+              // P, so that they follow one another without a pause.
+              if (kt < b) wait_k();
+              wait_v(kt);
+              if (kt == a) ok = ok && bar_wait(&bars->o_free[t], ((co++) & 1) ^ 1, abort_flag);
+              const uint64_t db = ptx::sdesc_advance(dv, v.s * C::KV_BYTES);
+              // O_t += P_t V, each half of the keys as soon as its P is there
+              ok = ok && bar_wait(&bars->p_full[t][0], cp, abort_flag);
               if (!ok) break;
               ptx::tc_fence_after();
-              issue_pv(s, first);
-              first = false;
-              if (it == b_t) ptx::mma_commit(&bars->o_done[t]);
-              ptx::mma_commit(&bars->kv_empty[s]);
-            } else {
-              ptx::mbar_arrive(&bars->kv_empty[s]);  // this tile does not use the stage
-            }
-            if (it + 1 <= U.u1) {
-              ok = bar_wait(&bars->k_full[slot(it + 1)], ring_par(it + 1), abort_flag);
+              ptx::mma_bf16_ts(tO, tS, db, idesc_o, kt != a);
+#pragma unroll
+              for (int kk = 1; kk < C::BK / 32; ++kk)
+                ptx::mma_bf16_ts(tO, tS + kk * 8, ptx::sdesc_advance(db, kk * (16 * 128)), idesc_o, 1);
+              ok = bar_wait(&bars->p_full[t][1], cp, abort_flag);
               if (!ok) break;
               ptx::tc_fence_after();
-              if (act(it + 1)) {
-                issue_s(slot(it + 1));
-                if (it + 1 == b_t) ptx::mma_commit(&bars->q_empty[t]);
+#pragma unroll
+              for (int kk = C::BK / 32; kk < C::BK / 16; ++kk)
+                ptx::mma_bf16_ts(tO, tS + kk * 8, ptx::sdesc_advance(db, kk * (16 * 128)), idesc_o, 1);
+              cp ^= 1;
+              if (kt < b) {
+                issue_s();
+                if (kt + 1 == b) ptx::mma_commit(&bars->q_empty[t]);
+              } else {
+                ptx::mma_commit(&bars->o_done[t]);
               }
+              ptx::mma_commit(&bars->v_empty[v.s]);
+              v.next();
             }
           }
-          g = g0 + (U.u1 - U.u0 + 1);
+          for (int kt = b + 1; ok && kt < w.t1; ++kt) skip(kt);
         }
         // Exit path: every MMA this thread issued has completed.
         ptx::mma_commit(&bars->drain[t]);
@@ -328,220 +415,142 @@ __global__ void __launch_bounds__(384, 1)
     const int t = warp / 4;               // Q tile of this warpgroup
     const int r = threadIdx.x - 128 * t;  // row within the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + C::tm_s(t);
-    const uint32_t tO = tmem + lane_base + C::tm_o(t);
+    const uint32_t tS = tmem + lane_base + C::tm_s(t), tO = tmem + lane_base + C::tm_o(t);
     const float c2 = p.scale_log2;
     int cs = 0, cd = 0, job = -1, followers = 0;
+    // The two warpgroups take turns at the exponentials, so that one's overlap
+    // the tensor core's work for the other (left to themselves they run side by
+    // side, share the special-function lanes and then wait for the tensor core
+    // together).  Order: (kt, tile 0), (kt, tile 1), (kt + 1, tile 0) ..; at every
+    // change of owner the finishing warpgroup arrives on the other's turn
+    // barrier.  Turns are passed and taken within a piece; a piece is begun when
+    // the other warpgroup is past its last turn of the piece before, so that no
+    // pass can run ahead of its take.
     int turns = 0;  // waits on this warpgroup's turn barrier so far
+    int n = 0;      // pieces so far
     bool ok = true;
-    while (ok && w.next()) {
+    for (; ok && w.next(); ++n) {
+      if (n > 0)
+        ok = __all_sync(0xffffffffu, bar_wait(&bars->done[1 - t][(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag));
+      if (!ok) break;
       const PagedItem& it = w.it;
-      const PagedTiles U = paged_tiles(p, w);
-      const int32_t lo = p.lo[it.hg], hi = p.hi[it.hg];
-      auto actv = [&](int tt, int kt) {
-        return tt ? (U.act[1] && kt >= U.a[1] && kt <= U.b[1]) : (U.act[0] && kt >= U.a[0] && kt <= U.b[0]);
-      };
-      const bool act_t = t ? U.act[1] : U.act[0];
-      const int a_t = t ? U.a[1] : U.a[0];
-      const int b_t = t ? U.b[1] : U.b[0];
-      const int rows_t = t ? U.rows[1] : U.rows[0];
-      const int64_t pos_first = t ? U.pos[1] : U.pos[0], pos_last = t ? U.last[1] : U.last[0];
-      const int64_t pos = pos_first + r / p.group;
-      const bool live = r < rows_t;
+      const PagedTile U = paged_tile(p, w, t), V = paged_tile(p, w, 1 - t);  // this tile, the other
+      const bool live = r < U.rows;
       if (!w.whole && w.begins) {
         job = w.item;
         followers = (int)((it.cost - w.len + plan.run.run - 1) / plan.run.run);
       }
-      const int64_t orow = paged_row(p, it, live ? t * 128 + r : 0);
-      float* slot = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D);
-      float* slot_ml = slot + C::ROWS * D + t * 128 + r;
-      if (!act_t) {
+      float* slot = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D) + (int64_t)(t * 128 + r) * D;
+      float* slot_ml = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D) + C::ROWS * D + t * 128 + r;
+      if (!U.active()) {
         // no key of this piece is attended to by this tile's rows
         if (live && w.whole) {
-          uint16_t* dst = p.o + orow * D;
+          const int64_t row = paged_row(p, it, t * 128 + r);
+          uint16_t* dst = p.o + row * D;
           for (int c = 0; c < D; c += 8) ptx::st_global_v4(dst + c, 0u, 0u, 0u, 0u);
-          p.lse[orow] = -INFINITY;
+          p.lse[row] = -INFINITY;
         } else if (live) {
           slot_ml[0] = -INFINITY;
           slot_ml[C::ROWS] = 0.f;
         }
+        ptx::mbar_arrive(&bars->done[t][n & 1]);
         continue;
+      }
+      // this row's permitted keys [row_lo, row_hi]; key tiles starting in
+      // [in_lo, in_hi] are permitted to every row of the tile
+      int row_lo, row_hi, in_lo, in_hi;
+      {
+        const int64_t lo = p.lo[it.hg], hi = p.hi[it.hg], pos = (int64_t)U.first_pos + r / p.group;
+        row_lo = (int)max64(pos - hi + 1, 0);
+        row_hi = live ? clamp_i32(min64(pos - lo, it.kv - 1)) : -1;
+        in_lo = (int)max64(U.last_pos - hi + 1, 0);
+        in_hi = clamp_i32(min64(U.first_pos - lo, it.kv - 1) - (C::BK - 1));
       }
       // Running max (base-2 units) and sum.  Rows that do not exist start as if
       // they had seen a key, so that their warp can take the fast path.
       float m_ref = live ? -INFINITY : 0.f, l = 0.f;
-      for (int kt = a_t; kt <= b_t; ++kt) {
-        int prev;
-        if (t == 1 && actv(0, kt)) prev = 0;
-        else if (actv(1, kt - 1)) prev = 1;
-        else if (actv(0, kt - 1)) prev = 0;
-        else prev = -1;  // a piece's first step waits for no turn
-        int nxt = -1;
-        if (t == 0 && actv(1, kt)) nxt = 1;
-        else if (actv(0, kt + 1)) nxt = 0;
-        else if (actv(1, kt + 1)) nxt = 1;  // and a piece's last step passes none
-        const bool pass_turn = nxt == 1 - t;
-        const int64_t j0 = (int64_t)kt * C::BK;
-        const bool interior = pos_first - (j0 + C::BK - 1) >= lo && pos_last - j0 < hi && j0 + C::BK <= it.kv;
-        // otherwise this row's permitted keys are the columns clo .. clo + span
-        int clo = 0;
-        uint32_t span = 127;
-        if (!interior) {
-          const int64_t c_first = max64(pos - hi + 1 - j0, 0);
-          const int64_t c_last = min64(min64(pos - lo - j0, it.kv - 1 - j0), 127);
-          if (!live || c_last < c_first) {
-            clo = 128;
-            span = 0;
-          } else {
-            clo = (int)c_first;
-            span = (uint32_t)(c_last - c_first);
-          }
-        }
-        const bool fast = __all_sync(0xffffffffu, m_ref != -INFINITY);
+      for (int kt = U.a; kt <= U.b; ++kt) {
+        const int other = kt + t;  // the next step's key tile if the other tile owns it
+        const bool take_turn = V.has(other - 1), pass_turn = V.has(other);
+        const int j0 = kt * C::BK;
         ok = __all_sync(0xffffffffu, bar_wait(&bars->s_full[t], (cs++) & 1, abort_flag));
         if (!ok) break;
-        if (TURN && prev == 1 - t)
-          ok = __all_sync(0xffffffffu, bar_wait(&bars->turn[t], (turns++) & 1, abort_flag));
-        if (!ok) break;
         ptx::tc_fence_after();
-        auto hand_turn = [&]() {
-          if (TURN && pass_turn) ptx::mbar_arrive(&bars->turn[1 - t]);
-        };
-        // Fast path, for every tile after a row's first: exponentiate against
-        // the current reference while tracking this tile's max; only if some
-        // row's max rose past the reference by more than 2^8 is the tile done
-        // again by the two-pass path (S is still intact then).
-        bool done = false;
-        if (fast) {
-          const float2 c2v = make_float2(c2, c2);
-          const float2 mnv = make_float2(-m_ref, -m_ref);
-          float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          uint32_t pk[2][32];
-          uint32_t sr[2][32];
-          ptx::tmem_ld32(tS, sr[0]);
-          ptx::tmem_wait_ld();
-          ptx::reg_fence(sr[0]);
-#define SPA_PAGED_FAST_CHUNKS(INTERIOR)                                                            \
-  _Pragma("unroll") for (int q = 0; q < 4; ++q) {                                                  \
-    if (q < 3) ptx::tmem_ld32(tS + (q + 1) * 32, sr[(q + 1) & 1]); /* next chunk in flight */      \
-    const uint32_t* cur = sr[q & 1];                                                               \
-    const int cb = q * 32 - clo;                                                                   \
-    _Pragma("unroll") for (int e = 0; e < 32; e += 4) {                                            \
-      float s0 = __uint_as_float(cur[e]), s1 = __uint_as_float(cur[e + 1]);                        \
-      float s2 = __uint_as_float(cur[e + 2]), s3 = __uint_as_float(cur[e + 3]);                    \
-      if (!(INTERIOR)) {                                                                           \
-        s0 = (uint32_t)(cb + e) <= span ? s0 : -INFINITY;                                          \
-        s1 = (uint32_t)(cb + e + 1) <= span ? s1 : -INFINITY;                                      \
-        s2 = (uint32_t)(cb + e + 2) <= span ? s2 : -INFINITY;                                      \
-        s3 = (uint32_t)(cb + e + 3) <= span ? s3 : -INFINITY;                                      \
-      }                                                                                            \
-      mx0 = ptx::fmax3(mx0, s0, s1);                                                               \
-      mx1 = ptx::fmax3(mx1, s2, s3);                                                               \
-      const float2 x01 = __ffma2_rn(make_float2(s0, s1), c2v, mnv);                                \
-      const float2 x23 = __ffma2_rn(make_float2(s2, s3), c2v, mnv);                                \
-      const float2 p01 = make_float2(ptx::exp2_approx(x01.x), ptx::exp2_approx(x01.y));            \
-      const float2 p23 = make_float2(ptx::exp2_approx(x23.x), ptx::exp2_approx(x23.y));            \
-      sa = __fadd2_rn(sa, p01);                                                                    \
-      sb = __fadd2_rn(sb, p23);                                                                    \
-      pk[q / 2][(q % 2) * 16 + e / 2] = E::pack(p01.x, p01.y);                                     \
-      pk[q / 2][(q % 2) * 16 + e / 2 + 1] = E::pack(p23.x, p23.y);                                 \
-    }                                                                                              \
-    if (q < 3) {                                                                                   \
-      ptx::tmem_wait_ld();                                                                         \
-      ptx::reg_fence(sr[(q + 1) & 1]);                                                             \
-    }                                                                                              \
-  }
-          if (interior) {
-            SPA_PAGED_FAST_CHUNKS(true)
-          } else {
-            SPA_PAGED_FAST_CHUNKS(false)
-          }
-#undef SPA_PAGED_FAST_CHUNKS
-          const bool over = live && fmaxf(mx0, mx1) * c2 > m_ref + 8.f;
-          if (!__any_sync(0xffffffffu, over)) {
-            hand_turn();
-            ptx::tmem_st32(tS, pk[0]);
-            ptx::tmem_st32(tS + 32, pk[1]);
-            l += (sa.x + sa.y) + (sb.x + sb.y);
-            done = true;
-          }
-        }
-        if (!done) {
-          // pass 1: row max of the raw scores (scale > 0 commutes with max)
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t sr[32];
-            ptx::tmem_ld32(tS + q * 32, sr);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence(sr);
-            const int cb = q * 32 - clo;
+        uint32_t s[4][32];  // the row's scores
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              mx0 = fmaxf(mx0, (uint32_t)(cb + e) <= span ? __uint_as_float(sr[e]) : -INFINITY);
-              mx1 = fmaxf(mx1, (uint32_t)(cb + e + 1) <= span ? __uint_as_float(sr[e + 1]) : -INFINITY);
-            }
-          }
-          const float m_new = fmaxf(m_ref, fmaxf(mx0, mx1) * c2);
-          const bool need = m_new > m_ref + 8.f;  // also true for a row's first finite max
-          const bool need_o = need && (m_ref != -INFINITY);
+        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(tS + q * 32, s[q]);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ptx::reg_fence(s[q]);
+        if (j0 < in_lo || j0 > in_hi) {
+          // the columns of this row's permitted keys: [row_lo - j0, row_hi - j0]
+#pragma unroll
+          for (int q = 0; q < 4; ++q) paged_mask32(s[q], row_lo - j0 - 32 * q, row_hi - j0 - 32 * q);
+        }
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            m4[q] = ptx::fmax3_nan(m4[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+        const float mx = ptx::fmax_nan(ptx::fmax3_nan(m4[0], m4[1], m4[2]), m4[3]) * c2;
+        // The reference moves when a row sees its first key, and afterwards only
+        // when the row's max rises past it by more than 2^8 (P stays below 2^8),
+        // so that O is rescaled rarely.  A row that has seen no key uses 0.
+        const bool moves = live && mx > m_ref + 8.f;  // also from -inf
+        if (mx != mx) l = mx;  // a score that is no number: nor are o and lse
+        if (__any_sync(0xffffffffu, moves)) {
           float alpha = 1.f;
-          if (need) {
-            alpha = ptx::exp2_approx(m_ref - m_new);  // 0 while the row had seen nothing
+          if (moves) {
+            alpha = ptx::exp2_approx(m_ref - mx);  // 0 while the row had seen nothing
+            m_ref = mx;
             l *= alpha;
-            m_ref = m_new;
           }
-          if (__any_sync(0xffffffffu, need_o)) {
-            // O_t is stable: the PV of the previous key tile completed before S_t did
-            const float a = need_o ? alpha : 1.f;
+          if (kt > U.a) {
+            // O_t is stable: the product before this tile completed before S_t did
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              ptx::tmem_ld32(tO + c, o);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              ptx::tmem_ld16(tO + c, o);
               ptx::tmem_wait_ld();
               ptx::reg_fence(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              ptx::tmem_st32(tO + c, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              ptx::tmem_st16(tO + c, o);
             }
           }
-          // pass 2: p = exp2(s * scale_log2 - m), pairs over the first half of
-          // S_t (chunk q of P covers columns [16q, 16q + 16), already read)
-          const float mneg = (m_ref == -INFINITY) ? 0.f : -m_ref;
-          float sm0 = 0.f, sm1 = 0.f;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t sr[32], pk[16];
-            ptx::tmem_ld32(tS + q * 32, sr);
-            ptx::tmem_wait_ld();
-            ptx::reg_fence(sr);
-            const int cb = q * 32 - clo;
+        }
+        if (take_turn) ok = __all_sync(0xffffffffu, bar_wait(&bars->turn[t], (turns++) & 1, abort_flag));
+        if (!ok) break;
+        // P over the first half of S, 16-bit pairs
+        const float mneg = m_ref == -INFINITY ? 0.f : -m_ref;
+        const float2 c2v = make_float2(c2, c2), mnv = make_float2(mneg, mneg);
+        float2 sa = make_float2(0.f, 0.f), sb = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float x0 = fmaf(__uint_as_float(sr[e]), c2, mneg), x1 = fmaf(__uint_as_float(sr[e + 1]), c2, mneg);
-              x0 = (uint32_t)(cb + e) <= span ? x0 : -INFINITY;
-              x1 = (uint32_t)(cb + e + 1) <= span ? x1 : -INFINITY;
-              const float p0 = ptx::exp2_approx(x0), p1 = ptx::exp2_approx(x1);
-              sm0 += p0;
-              sm1 += p1;
-              pk[e / 2] = E::pack(p0, p1);
-            }
-            ptx::tmem_st16(tS + q * 16, pk);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+          paged_exp32<E>(s[q], c2v, mnv, sa, sb, pk);
+          if (q == 2) {  // the first half has been stored meanwhile
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&bars->p_full[t][0]);
           }
-          l += sm0 + sm1;
-          hand_turn();
+          if (q == 3 && pass_turn) ptx::mbar_arrive(&bars->turn[1 - t]);
+          ptx::tmem_st16(tS + q * 16, pk);
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(&bars->p_full[t]);
+        ptx::mbar_arrive(&bars->p_full[t][1]);
+        l += (sa.x + sa.y) + (sb.x + sb.y);
       }
       if (!ok) break;
+      ptx::mbar_arrive(&bars->done[t][n & 1]);
       // ---------------------------------------------------------- epilogue
       ok = __all_sync(0xffffffffu, bar_wait(&bars->o_done[t], (cd++) & 1, abort_flag));
       if (!ok) break;
       ptx::tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t row = paged_row(p, it, live ? t * 128 + r : 0);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -549,17 +558,16 @@ __global__ void __launch_bounds__(384, 1)
         ptx::tmem_wait_ld();
         ptx::reg_fence(o);
         if (live && w.whole) {
-          store_row32<E>(p.o + orow * D + c, o, inv);
+          store_row32<E>(p.o + row * D + c, o, inv);
         } else if (live) {
-          float* dst = slot + (int64_t)(t * 128 + r) * D + c;
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) ptx::st_global_v8(dst + e, o + e);
+          for (int e = 0; e < 32; e += 8) ptx::st_global_v8(slot + c + e, o + e);
         }
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive(&bars->o_free[t]);
       if (live && w.whole) {
-        p.lse[orow] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
+        p.lse[row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       } else if (live) {
         slot_ml[0] = m_ref;
         slot_ml[C::ROWS] = l;

@@ -866,13 +866,8 @@ int make_paged_q_map(CUtensorMap* m, const spa::PagedParams& p, int d, int dtype
 template <class E, int D>
 int paged_long_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
   using C = spa::PagedLongCfg<D>;
-  static std::atomic<uint64_t> prepared[2];
-  static std::atomic<int> regs_ok[2];
-  // the softmax warpgroups take turns when the bands are wide on average (the
-  // forward's rule, kFwdTurnMinWidth)
-  int64_t width_sum = 0;
-  for (int g = 0; g < p.ng; ++g) width_sum += (int64_t)p.hi[g] - p.lo[g];
-  const bool turn = width_sum >= kFwdTurnMinWidth * (int64_t)p.ng;
+  static std::atomic<uint64_t> prepared;
+  static std::atomic<int> regs_ok;
   CUtensorMap mq, mk, mv;
   int st;
   const int rows = std::min(c.page, C::TK);
@@ -880,12 +875,12 @@ int paged_long_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
       (st = make_page_map(&mk, c.k_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)) ||
       (st = make_page_map(&mv, c.v_pages, p.pages, p.Hk, c.page, D, rows, c.dtype)))
     return st;
-  auto* kernel = turn ? spa::spa_paged_long_kernel<E, D, true> : spa::spa_paged_long_kernel<E, D, false>;
-  if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared[turn]))) return st;
-  if ((st = check_regs(kernel, (int)C::LAUNCH_REGS, regs_ok[turn]))) return st;
+  auto* kernel = spa::spa_paged_long_kernel<E, D>;
+  if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
+  if ((st = check_regs(kernel, (int)C::LAUNCH_REGS, regs_ok))) return st;
   kernel<<<kPagedLongCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mq, mk, mv, p);
   if ((st = launch_status())) return st;
-  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedLongCtas, 8, s);
+  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedLongCtas, 64, s);
 }
 
 // Groups the query heads into work items of `group` heads (a divisor of the
