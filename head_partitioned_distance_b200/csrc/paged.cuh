@@ -10,14 +10,15 @@
 //
 // Work list.  An item is (sequence, head group, row block); a head group is
 // `group` query heads that share a key/value head and, when group > 1, one
-// band, so that each key is fetched once for all of them.  An item costs as
-// many steps as it has key tiles.  All items laid end to end form one line of
-// steps that the CTAs cut into equal runs: sequences of any mixture of lengths
-// load every SM alike, and a long sequence with few rows is spread over many
-// SMs.  An item that a cut divides leaves one partial (fp32 o, running max and
-// sum) per run, which the merge kernel joins; the others write their rows
-// directly.  Every CTA derives its run from the lengths on the device, so the
-// host needs none of them and a captured call follows them.
+// band, so that each key is fetched once for all of them.  All items laid end
+// to end, each as long as its key tiles plus what beginning and ending a piece
+// costs, form one line that is cut into equal runs, one per CTA: sequences of
+// any mixture of lengths load every SM alike, and a long sequence with few
+// rows is spread over many SMs.  A plan kernel finds the cuts from the lengths
+// on the device, so the host needs none of them and a captured call follows
+// them.  An item that a cut divides leaves one partial (fp32 o, running max
+// and sum) per piece; whoever leaves the last joins them all, in their order,
+// so the result does not depend on which was last.
 #pragma once
 
 #include "common.cuh"
@@ -32,7 +33,8 @@ struct PagedParams {
   const uint16_t* q;  // [T][Hq][d]
   uint16_t* o;        // [T][Hq][d]
   float* lse;         // [T][Hq]
-  int32_t* desc;      // per CTA: item it began and did not finish (or -1), CTAs that follow
+  int4* plan;         // PagedCut of every CTA and of the end
+  int32_t* arrived;   // pieces that have left their partial, by the CTA that began the item (x 2 row halves)
   float* part;        // two partial slots per CTA
   int64_t pages;
   int B, T, Hq, max_q;
@@ -43,8 +45,10 @@ struct PagedParams {
   int nblk;           // row blocks per (sequence, head group)
   int blk_tokens;     // tokens per row block
   int width, page_shift;
-  int min_run;        // steps per CTA, at least
-  int max_split;      // runs an item is cut into, about
+  int ctas;           // runs the line is cut into, at most
+  int piece_cost;     // cost of a piece besides its key tiles, in key tiles
+  int min_run;        // length of a run, at least
+  int max_split;      // pieces of an item, about
   float scale_log2;
   int32_t lo[kMaxHeads];  // per head group
   int32_t hi[kMaxHeads];
@@ -58,7 +62,7 @@ struct PagedItem {
   int jlo, jhi;  // keys that some row attends to (jhi < jlo: none)
   int kv;        // keys the sequence has (and the page table can name)
   int t0;        // first key tile
-  int cost;      // steps; an item without keys takes one
+  int cost;      // key tiles; an item without keys counts one
 };
 
 // Positions and lengths are 32-bit; sums of them with band limits need more.
@@ -92,30 +96,36 @@ __device__ __forceinline__ PagedItem paged_item_at(const PagedParams& p, int ite
   return paged_item<TK>(p, rest / p.ng, rest % p.ng, blk);
 }
 
-// This CTA's run of steps.
-struct PagedRun {
-  long long s0, s1;  // [s0, s1) of the line
-  long long run;     // steps per CTA
-  int item, off;     // item that holds step s0, and the steps of it before s0
+// Where a CTA's run begins: key tile `off` of an item (0: the item is whole
+// from there on).  off > 0: CTA `head` began the item, which has `pieces`.
+struct PagedCut {
+  int item, off, head, pieces;
 };
 
-struct PagedPlanSmem {
-  long long sum[32];
-  int most[32];
-  PagedRun run;
-};
+constexpr int kPagedPlanThreads = 1024;
+constexpr int kPagedMaxCtas = 296;
 
-// Called by all NT threads of the CTA; ends with a barrier.
-template <int TK, int NT>
-__device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlanSmem& sm) {
+// One CTA.  Cuts the line into ctas runs and clears the arrival counts.
+template <int TK>
+__global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ long long s_sum[32];
+  __shared__ int s_most[32];
+  __shared__ long long s_before[kPagedPlanThreads + 1];  // line before each thread's items
+  __shared__ int s_item[kPagedMaxCtas + 1], s_off[kPagedMaxCtas + 1];
+  // the kernel that follows may be launched: it waits for this one to end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int items = p.B * p.ng * p.nblk;
-  const int per = (items + NT - 1) / NT;
+  const int per = (items + kPagedPlanThreads - 1) / kPagedPlanThreads;
   const int i0 = min((int)threadIdx.x * per, items), i1 = min(i0 + per, items);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto length = [&](int i) {
+    const int c = paged_item_at<TK>(p, i).cost;
+    return c ? c + p.piece_cost : 0;
+  };
   long long mine = 0;
   int most = 0;
   for (int i = i0; i < i1; ++i) {
-    const int c = paged_item_at<TK>(p, i).cost;
+    const int c = length(i);
     mine += c;
     most = max(most, c);
   }
@@ -126,87 +136,112 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, PagedPlanSmem& 
     if (lane >= m) incl += v;
     most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
   }
-  if (lane == 31) sm.sum[warp] = incl;
-  if (lane == 0) sm.most[warp] = most;
-  if (threadIdx.x == 0) {
-    sm.run.item = items;
-    sm.run.off = 0;
-  }
+  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 0) s_most[warp] = most;
+  for (int c = threadIdx.x; c < 2 * p.ctas; c += kPagedPlanThreads) p.arrived[c] = 0;
   __syncthreads();
   long long before = incl - mine, total = 0;
   most = 0;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += sm.sum[w];
-    total += sm.sum[w];
-    most = max(most, sm.most[w]);
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+    most = max(most, s_most[w]);
   }
-  long long run = (total + gridDim.x - 1) / gridDim.x;
+  s_before[threadIdx.x] = before;
+  if (threadIdx.x == 0) s_before[kPagedPlanThreads] = total;
+  __syncthreads();
+  long long run = (total + p.ctas - 1) / p.ctas;
   run = max(run, (long long)((most + p.max_split - 1) / p.max_split));
   run = max(run, (long long)p.min_run);
-  const long long s0 = min(run * blockIdx.x, total), s1 = min(s0 + run, total);
-  if (s0 < s1 && before <= s0 && s0 < before + mine) {
-    long long at = before;
-    for (int i = i0; i < i1; ++i) {
-      const int c = paged_item_at<TK>(p, i).cost;
-      if (at + c > s0) {
-        sm.run.item = i;
-        sm.run.off = (int)(s0 - at);
-        break;
+  if ((int)threadIdx.x <= p.ctas) {
+    // the item that holds place run * c of the line, by bisection over the
+    // threads' shares, then within the share
+    const long long at = run * threadIdx.x;
+    int item = items, off = 0;
+    if (at < total) {
+      int a = 0, b = kPagedPlanThreads;  // s_before[a] <= at < s_before[b]
+      while (b - a > 1) {
+        const int m = (a + b) / 2;
+        if (s_before[m] <= at) a = m;
+        else b = m;
       }
-      at += c;
+      long long x = s_before[a];
+      item = min(a * per, items);
+      int c = length(item);
+      while (x + c <= at) {
+        x += c;
+        c = length(++item);
+      }
+      // a piece of no or one key tile is not worth its beginning: the cut moves
+      // to the item's start or end
+      off = (int)(at - x) - p.piece_cost;
+      if (off < 2) off = 0;
+      else if (c - p.piece_cost - off < 2) ++item, off = 0;
     }
-  }
-  if (threadIdx.x == 0) {
-    sm.run.s0 = s0;
-    sm.run.s1 = s1;
-    sm.run.run = run;
+    s_item[threadIdx.x] = item;
+    s_off[threadIdx.x] = off;
   }
   __syncthreads();
+  if ((int)threadIdx.x <= p.ctas) {
+    const int c = threadIdx.x, item = s_item[c], off = s_off[c];
+    int first = c, last = c;  // the cuts within this item
+    if (off > 0) {
+      while (first > 0 && s_item[first - 1] == item && s_off[first - 1] > 0) --first;
+      while (last < p.ctas && s_item[last + 1] == item && s_off[last + 1] > 0) ++last;
+    }
+    p.plan[c] = make_int4(item, off, first - 1, last - first + 2);
+  }
 }
 
-// The pieces of a CTA's run, in order: tiles [t0, t1) of one item each.
+// This CTA's run: from its cut to the next.
+struct PagedRun {
+  PagedCut from, to;
+  __device__ __forceinline__ explicit PagedRun(const PagedParams& p) {
+    const int4 a = p.plan[blockIdx.x], b = p.plan[blockIdx.x + 1];
+    from = {a.x, a.y, a.z, a.w};
+    to = {b.x, b.y, b.z, b.w};
+  }
+};
+
+// The pieces of a CTA's run, in order: key tiles [t0, t1) of one item each.
 template <int TK>
 struct PagedWalk {
   const PagedParams& p;
-  long long left;
-  int item, off;
+  const PagedRun run;
+  int item;
   PagedItem it;
-  int t0, t1;     // key tiles of this piece (none for an item without keys)
-  int len;        // steps
-  bool whole;     // the piece is the whole item
-  bool begins;    // it holds the item's first step
-  __device__ __forceinline__ PagedWalk(const PagedParams& pp, const PagedRun& r)
-      : p(pp), left(r.s1 - r.s0), item(r.item - 1), off(r.off) {}
+  int t0, t1;   // key tiles of this piece (none for an item without keys)
+  bool whole;   // the piece is the whole item
+  bool begins;  // it holds the item's first key tile
+  __device__ __forceinline__ PagedWalk(const PagedParams& pp, const PagedRun& r) : p(pp), run(r), item(r.from.item - 1) {}
   __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
     do {
-      it = paged_item_at<TK>(p, ++item);
+      ++item;
+      if (item > run.to.item || (item == run.to.item && run.to.off == 0)) return false;
+      it = paged_item_at<TK>(p, item);
     } while (it.cost == 0);
-    len = (int)min((long long)(it.cost - off), left);
-    whole = len == it.cost;
+    const int off = item == run.from.item ? run.from.off : 0;
+    const int end = item == run.to.item ? run.to.off : it.cost;
     begins = off == 0;
+    whole = begins && end == it.cost;
     t0 = it.t0 + off;
-    t1 = it.jhi < it.jlo ? t0 : t0 + len;
-    left -= len;
-    off = 0;
+    t1 = it.jhi < it.jlo ? t0 : it.t0 + end;
     return true;
   }
+  // of a piece that is not the whole item: who began the item, its pieces
+  __device__ __forceinline__ int head() const { return begins ? (int)blockIdx.x : run.from.head; }
+  __device__ __forceinline__ int pieces() const { return begins ? run.to.pieces : run.from.pieces; }
 };
 
 // Partial of `rows` rows: o [rows][d], then the maxima (base 2) and the sums.
 __host__ __device__ constexpr int64_t paged_slot_floats(int rows, int d) { return (int64_t)rows * (d + 2); }
 
-// A CTA's partials: a piece that ends an item begun by an earlier CTA (or lies
-// inside it) goes to slot 2c, one that begins an item to slot 2c + 1.
-__device__ __forceinline__ float* paged_slot(const PagedParams& p, int cta, bool begins, int rows, int d) {
-  return p.part + (2 * (int64_t)cta + (begins ? 1 : 0)) * paged_slot_floats(rows, d);
-}
-
-// What the merge has to do for the item this CTA began (one thread).
-__device__ __forceinline__ void paged_describe(const PagedParams& p, int item, int followers) {
-  p.desc[2 * blockIdx.x] = item;
-  p.desc[2 * blockIdx.x + 1] = followers;
+// A CTA's partials: the piece that begins an item goes to slot 2c + 1, one that
+// goes on with an item begun by an earlier CTA to slot 2c.  Piece i of an item
+// that CTA `head` began:
+__device__ __forceinline__ float* paged_slot(const PagedParams& p, int head, int i, int rows, int d) {
+  return p.part + (i ? 2 * ((int64_t)head + i) : 2 * (int64_t)head + 1) * paged_slot_floats(rows, d);
 }
 
 // Token row and head of row r of an item.
@@ -230,17 +265,16 @@ struct PagedShortCfg {
   static constexpr uint32_t KV_BYTES = TK * D * 2, STAGE_BYTES = 2 * KV_BYTES;
   static constexpr uint32_t OFF_RED = NS * STAGE_BYTES;          // [WARPS][4 rows][D] fp32
   static constexpr uint32_t OFF_ML = OFF_RED + WARPS * 4 * D * 4;  // [2][WARPS][ROWS] fp32
-  static constexpr uint32_t OFF_PLAN = OFF_ML + 2 * WARPS * ROWS * 4;
-  static constexpr uint32_t OFF_BAR = OFF_PLAN + 512;
+  static constexpr uint32_t OFF_BAR = OFF_ML + 2 * WARPS * ROWS * 4;
   static constexpr uint32_t USED = OFF_BAR + 256;
   static constexpr uint32_t SMEM_BYTES = USED + 1024;  // alignment slack
-  static_assert(sizeof(PagedPlanSmem) <= 512, "plan space");
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 struct PagedShortBars {
   uint64_t full[6], empty[6];
   int abort;
+  int last;  // this CTA's piece was its item's last to arrive
 };
 
 template <class E>
@@ -302,6 +336,50 @@ struct PagedPages {
   }
 };
 
+// One warp joins row r of an item from its pieces' partials, in their order:
+//   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  lse = M + log2 of it.
+template <class E, int D, int ROWS>
+__device__ __forceinline__ void paged_join_row(const PagedParams& p, int head, int pieces, int r, int64_t row) {
+  constexpr int CW = D / 32;
+  const int lane = threadIdx.x % 32;
+  float mx = -INFINITY;
+  for (int i = lane; i < pieces; i += 32) mx = ptx::fmax_nan(mx, paged_slot(p, head, i, ROWS, D)[ROWS * D + r]);
+#pragma unroll
+  for (int k = 16; k > 0; k /= 2) mx = ptx::fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+  float sum = 0.f, out[CW] = {};
+  for (int i0 = 0; i0 < pieces; i0 += 32) {
+    const int i = i0 + lane;
+    float f = 0.f, li = 0.f;
+    if (i < pieces) {
+      const float* ml = paged_slot(p, head, i, ROWS, D) + ROWS * D + r;
+      f = ml[0] == -INFINITY ? 0.f : ptx::exp2_approx(ml[0] - mx);
+      li = ml[ROWS] * f;
+    }
+#pragma unroll 4
+    for (int k = 0; k < min(32, pieces - i0); ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      sum += __shfl_sync(0xffffffffu, li, k);
+      const float* src = paged_slot(p, head, i0 + k, ROWS, D) + r * D + lane * CW;
+      float v[CW];
+      if constexpr (CW == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(src);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(src);
+        v[0] = u.x; v[1] = u.y;
+      }
+      // a piece in which the row attends to nothing counts for nothing
+#pragma unroll
+      for (int e = 0; e < CW; ++e) out[e] = fk == 0.f ? out[e] : fmaf(fk, v[e], out[e]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (CW / 2);
+#pragma unroll
+  for (int e = 0; e < CW / 2; ++e) dst[e] = E::pack(out[2 * e] * inv, out[2 * e + 1] * inv);
+  if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
 template <class E, int D>
 __global__ void __launch_bounds__(160, 2)
     spa_paged_short_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -311,7 +389,6 @@ __global__ void __launch_bounds__(160, 2)
   uint8_t* smem = align1024(smem_raw);
   if (!smem_fits(smem_raw, smem, C::USED)) return;
   PagedShortBars* bars = reinterpret_cast<PagedShortBars*>(smem + C::OFF_BAR);
-  PagedPlanSmem& plan = *reinterpret_cast<PagedPlanSmem*>(smem + C::OFF_PLAN);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -323,11 +400,10 @@ __global__ void __launch_bounds__(160, 2)
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
   }
-  paged_plan<C::TK, C::NTHREADS>(p, plan);
-  // the merge kernel may start its launch: it waits for this grid to finish
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   volatile int* abort_flag = &bars->abort;
-  PagedWalk<C::TK> w(p, plan.run);
+  PagedWalk<C::TK> w(p, PagedRun(p));
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ TMA producer
@@ -375,7 +451,7 @@ __global__ void __launch_bounds__(160, 2)
   float* s_m = reinterpret_cast<float*>(smem + C::OFF_ML);
   float* s_l = s_m + C::WARPS * C::ROWS;
   const int quad = lane / 4, qc = lane % 4;
-  int g = 0, job = -1, followers = 0;
+  int g = 0;
   // A warp whose wait runs out of time computes no further tile, but walks on
   // through the pieces, so that the named barriers keep their four warps.
   bool ok = true;
@@ -505,7 +581,8 @@ __global__ void __launch_bounds__(160, 2)
       for (int y = 1; y < C::WARPS; ++y) mx = ptx::fmax_nan(mx, s_m[y * C::ROWS + quad + 8 * x]);
       f[x] = m[x] == -INFINITY ? 0.f : ptx::exp2_approx(m[x] - mx);
     }
-    float* slot = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D);
+    const int head = w.whole ? 0 : w.head(), piece = blockIdx.x - head;
+    float* slot = paged_slot(p, head, piece, C::ROWS, D);
     for (int r0 = 0; r0 < rows; r0 += 4) {
       const int x = r0 / 8;  // these four rows are the lanes' first or second
       if (quad - r0 % 8 >= 0 && quad - r0 % 8 < 4) {
@@ -548,70 +625,17 @@ __global__ void __launch_bounds__(160, 2)
       }
       ptx::named_bar_sync(1, C::WARPS * 32);
     }
-    if (!w.whole && w.begins) {
-      job = w.item;
-      followers = (int)((it.cost - w.len + plan.run.run - 1) / plan.run.run);
-    }
-  }
-  if (threadIdx.x == 0) paged_describe(p, ok ? job : -1, followers);
-}
-
-// ------------------------------------------------------------------ merge
-// CTA x joins the partials of the item that CTA x of the main kernel began
-// and left unfinished: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over
-// its pieces, in their order.  One warp per row; grid y shares the rows.
-template <class E, int D, int ROWS, int TK>
-__global__ void __launch_bounds__(128) spa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int item = p.desc[2 * c], n = p.desc[2 * c + 1] + 1;
-  // (a CTA of the main kernel that could not run has described nothing)
-  if (item < 0 || item >= p.B * p.ng * p.nblk || n < 1 || c + n > (int)gridDim.x) return;
-  constexpr int CW = D / 32;
-  constexpr int64_t SLOT = paged_slot_floats(ROWS, D);
-  const PagedItem it = paged_item_at<TK>(p, item);
-  const int rows = it.tokens * p.group;
-  // piece 0 lies in slot 2c + 1, piece i in slot 2 (c + i)
-  const float* base = p.part + 2 * (int64_t)c * SLOT;
-  for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
-    float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32)
-      mx = ptx::fmax_nan(mx, base[(i ? 2 * i : 1) * SLOT + ROWS * D + r]);
-#pragma unroll
-    for (int k = 16; k > 0; k /= 2) mx = ptx::fmax_nan(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    float sum = 0.f, out[CW] = {};
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane;
-      float f = 0.f, li = 0.f;
-      if (i < n) {
-        const float* ml = base + (i ? 2 * i : 1) * SLOT + ROWS * D + r;
-        f = ml[0] == -INFINITY ? 0.f : ptx::exp2_approx(ml[0] - mx);
-        li = ml[ROWS] * f;
-      }
-#pragma unroll 4
-      for (int k = 0; k < min(32, n - i0); ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        sum += __shfl_sync(0xffffffffu, li, k);
-        const float* src = base + (i0 + k ? 2 * (i0 + k) : 1) * SLOT + r * D + lane * CW;
-        float v[CW];
-        if constexpr (CW == 4) {
-          const float4 u = *reinterpret_cast<const float4*>(src);
-          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-        } else {
-          const float2 u = *reinterpret_cast<const float2*>(src);
-          v[0] = u.x; v[1] = u.y;
-        }
-        // a piece in which the row attends to nothing counts for nothing
-#pragma unroll
-        for (int e = 0; e < CW; ++e) out[e] = fk == 0.f ? out[e] : fmaf(fk, v[e], out[e]);
+    if (!w.whole) {
+      // whoever leaves the item's last partial joins them all
+      __threadfence();
+      ptx::named_bar_sync(1, C::WARPS * 32);
+      if (threadIdx.x == 0) bars->last = atomicAdd(&p.arrived[2 * head], 1) == w.pieces() - 1;
+      ptx::named_bar_sync(1, C::WARPS * 32);
+      if (bars->last) {
+        __threadfence();
+        for (int r = warp; r < rows; r += C::WARPS) paged_join_row<E, D, C::ROWS>(p, head, w.pieces(), r, paged_row(p, it, r));
       }
     }
-    const int64_t row = paged_row(p, it, r);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (CW / 2);
-#pragma unroll
-    for (int e = 0; e < CW / 2; ++e) dst[e] = E::pack(out[2 * e] * inv, out[2 * e + 1] * inv);
-    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
   }
 }
 

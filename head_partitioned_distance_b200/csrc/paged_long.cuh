@@ -40,8 +40,7 @@ struct PagedLongCfg {
   static constexpr uint32_t OFF_K = OFF_Q + 2 * Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_V + NV * KV_BYTES;
-  static constexpr uint32_t OFF_PLAN = OFF_BAR + 384;
-  static constexpr uint32_t USED = OFF_PLAN + 512;
+  static constexpr uint32_t USED = OFF_BAR + 384;
   // at least 116 KB, so that one CTA (and its 512 TMEM columns) owns an SM
   static constexpr uint32_t SMEM_BYTES = USED + 1024 > 116u * 1024 ? USED + 1024 : 116u * 1024;
   static_assert(SMEM_BYTES <= kMaxSmemPerBlock, "shared memory");
@@ -65,9 +64,11 @@ struct PagedLongBars {
   uint64_t o_done[2], o_free[2];
   uint64_t turn[2];       // turn[t]: softmax warpgroup t may form its exponentials
   uint64_t done[2][2];    // done[t][piece % 2]: warpgroup t is past its last turn of the piece
+  uint64_t meet[2];       // warpgroup t's threads
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort;
+  int last[2];            // warpgroup t's partial was its item's last to arrive
 };
 static_assert(sizeof(PagedLongBars) <= 384, "barrier space");
 
@@ -143,6 +144,42 @@ __device__ __forceinline__ void paged_exp32(const uint32_t (&s)[32], float2 c2v,
   }
 }
 
+// One thread joins row r of an item from its pieces' partials, in their order
+// (paged_join_row's sums over the layout of this kernel's partials).
+template <class E, int D, int ROWS>
+__device__ __forceinline__ void paged_join_thread(const PagedParams& p, int head, int pieces, int r, int64_t row) {
+  float mx = -INFINITY;
+  for (int i = 0; i < pieces; ++i) mx = ptx::fmax_nan(mx, paged_slot(p, head, i, ROWS, D)[ROWS * D + r]);
+  float sum = 0.f, out[D];
+#pragma unroll
+  for (int e = 0; e < D; ++e) out[e] = 0.f;
+  for (int i = 0; i < pieces; ++i) {
+    const float* slot = paged_slot(p, head, i, ROWS, D);
+    const float m = slot[ROWS * D + r];
+    if (m == -INFINITY) continue;  // the row attends to nothing in this piece
+    const float f = ptx::exp2_approx(m - mx);
+    sum = fmaf(slot[ROWS * D + ROWS + r], f, sum);
+#pragma unroll
+    for (int e = 0; e < D; e += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(slot + (e / 8) * (8 * ROWS) + r * 8 + e % 8);
+      out[e] = fmaf(f, v.x, out[e]);
+      out[e + 1] = fmaf(f, v.y, out[e + 1]);
+      out[e + 2] = fmaf(f, v.z, out[e + 2]);
+      out[e + 3] = fmaf(f, v.w, out[e + 3]);
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint16_t* dst = p.o + row * D;
+#pragma unroll
+  for (int c = 0; c < D; c += 32) {
+    uint32_t g[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) g[e] = __float_as_uint(out[c + e]);
+    store_row32<E>(dst + c, g, inv);
+  }
+  p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
+}
+
 template <class E, int D>
 __global__ void __launch_bounds__(384, 1)
     spa_paged_long_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -152,7 +189,6 @@ __global__ void __launch_bounds__(384, 1)
   uint8_t* smem = align1024(smem_raw);
   if (!smem_fits(smem_raw, smem, C::USED)) return;
   PagedLongBars* bars = reinterpret_cast<PagedLongBars*>(smem + C::OFF_BAR);
-  PagedPlanSmem& plan = *reinterpret_cast<PagedPlanSmem*>(smem + C::OFF_PLAN);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t sQ = ptx::smem_u32(smem + C::OFF_Q);
   const uint32_t sK = ptx::smem_u32(smem + C::OFF_K);
@@ -170,6 +206,7 @@ __global__ void __launch_bounds__(384, 1)
       ptx::mbar_init(&bars->turn[i], 128);
       ptx::mbar_init(&bars->done[i][0], 128);
       ptx::mbar_init(&bars->done[i][1], 128);
+      ptx::mbar_init(&bars->meet[i], 128);
       ptx::mbar_init(&bars->drain[i], 1);
     }
     for (int i = 0; i < C::NK; ++i) {
@@ -194,12 +231,12 @@ __global__ void __launch_bounds__(384, 1)
     ptx::prefetch_tmap(&tm_v);
   }
   ptx::tc_fence_before();
-  paged_plan<C::TK, C::NTHREADS>(p, plan);
+  __syncthreads();
   ptx::tc_fence_after();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
-  PagedWalk<C::TK> w(p, plan.run);
+  PagedWalk<C::TK> w(p, PagedRun(p));
 
   if (warp >= 8) {
     ptx::regs_dec<C::CONTROL_REGS>();
@@ -417,7 +454,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_base = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t tS = tmem + lane_base + C::tm_s(t), tO = tmem + lane_base + C::tm_o(t);
     const float c2 = p.scale_log2;
-    int cs = 0, cd = 0, job = -1, followers = 0;
+    int cs = 0, cd = 0, met = 0;
     // The two warpgroups take turns at the exponentials, so that one's overlap
     // the tensor core's work for the other (left to themselves they run side by
     // side, share the special-function lanes and then wait for the tensor core
@@ -436,16 +473,28 @@ __global__ void __launch_bounds__(384, 1)
       const PagedItem& it = w.it;
       const PagedTile U = paged_tile(p, w, t), V = paged_tile(p, w, 1 - t);  // this tile, the other
       const bool live = r < U.rows;
-      if (!w.whole && w.begins) {
-        job = w.item;
-        followers = (int)((it.cost - w.len + plan.run.run - 1) / plan.run.run);
-      }
-      float* slot = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D) + (int64_t)(t * 128 + r) * D;
-      float* slot_ml = paged_slot(p, blockIdx.x, w.begins, C::ROWS, D) + C::ROWS * D + t * 128 + r;
+      // this row's place in a partial: 8 columns of all rows after one another,
+      // so that 32 rows' 32-byte vectors lie side by side
+      const int head = w.whole ? 0 : w.head();
+      float* slot = paged_slot(p, head, blockIdx.x - head, C::ROWS, D) + (t * 128 + r) * 8;
+      float* slot_ml = paged_slot(p, head, blockIdx.x - head, C::ROWS, D) + C::ROWS * D + t * 128 + r;
+      const int64_t row = paged_row(p, it, live ? t * 128 + r : 0);
+      // leaves the item's partial; whoever leaves the last joins them all
+      auto leave = [&]() {
+        __threadfence();
+        ptx::mbar_arrive(&bars->meet[t]);
+        ok = __all_sync(0xffffffffu, bar_wait(&bars->meet[t], (met++) & 1, abort_flag));
+        if (ok && r == 0) bars->last[t] = atomicAdd(&p.arrived[2 * head + t], 1) == w.pieces() - 1;
+        ptx::mbar_arrive(&bars->meet[t]);
+        ok = __all_sync(0xffffffffu, ok && bar_wait(&bars->meet[t], (met++) & 1, abort_flag));
+        if (!ok || !*(volatile int*)&bars->last[t]) return;
+        __threadfence();
+        if (live) paged_join_thread<E, D, C::ROWS>(p, head, w.pieces(), t * 128 + r, row);
+      };
       if (!U.active()) {
         // no key of this piece is attended to by this tile's rows
+        ptx::mbar_arrive(&bars->done[t][n & 1]);
         if (live && w.whole) {
-          const int64_t row = paged_row(p, it, t * 128 + r);
           uint16_t* dst = p.o + row * D;
           for (int c = 0; c < D; c += 8) ptx::st_global_v4(dst + c, 0u, 0u, 0u, 0u);
           p.lse[row] = -INFINITY;
@@ -453,7 +502,7 @@ __global__ void __launch_bounds__(384, 1)
           slot_ml[0] = -INFINITY;
           slot_ml[C::ROWS] = 0.f;
         }
-        ptx::mbar_arrive(&bars->done[t][n & 1]);
+        if (!w.whole) leave();
         continue;
       }
       // this row's permitted keys [row_lo, row_hi]; key tiles starting in
@@ -550,7 +599,6 @@ __global__ void __launch_bounds__(384, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t row = paged_row(p, it, live ? t * 128 + r : 0);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -561,7 +609,7 @@ __global__ void __launch_bounds__(384, 1)
           store_row32<E>(p.o + row * D + c, o, inv);
         } else if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) ptx::st_global_v8(slot + c + e, o + e);
+          for (int e = 0; e < 32; e += 8) ptx::st_global_v8(slot + (c + e) * C::ROWS, o + e);
         }
       }
       ptx::tc_fence_before();
@@ -569,11 +617,11 @@ __global__ void __launch_bounds__(384, 1)
       if (live && w.whole) {
         p.lse[row] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994531f;
       } else if (live) {
-        slot_ml[0] = m_ref;
+        slot_ml[0] = l == l ? m_ref : l;  // (no number stays seen)
         slot_ml[C::ROWS] = l;
       }
+      if (!w.whole) leave();
     }
-    if (threadIdx.x == 0) paged_describe(p, ok ? job : -1, followers);
   }
 
   ptx::tc_fence_before();

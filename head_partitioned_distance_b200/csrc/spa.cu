@@ -801,11 +801,14 @@ int make_page_map(CUtensorMap* m, const void* ptr, int64_t pages, int Hk, int pa
 }
 
 // CTAs of the kernel for few rows: two on each of a B200's 148 SMs.  Each has
-// two partial slots in the workspace, after the merge's descriptions.
+// two partial slots in the workspace.
 // The kernel for many rows has one CTA per SM.
 constexpr int kPagedShortCtas = 296, kPagedLongCtas = 148;
-constexpr size_t kPagedDescBytes = 4096;
-static_assert(kPagedShortCtas * 2 * sizeof(int32_t) <= kPagedDescBytes, "descriptions");
+// workspace: the plan's cuts, the arrival counts, the partials
+constexpr size_t kPagedPlanBytes = 5120, kPagedHeadBytes = kPagedPlanBytes + 3072;
+static_assert(kPagedShortCtas <= spa::kPagedMaxCtas && kPagedLongCtas <= spa::kPagedMaxCtas, "runs");
+static_assert((spa::kPagedMaxCtas + 1) * sizeof(int4) <= kPagedPlanBytes, "cuts");
+static_assert(2 * spa::kPagedMaxCtas * sizeof(int32_t) <= kPagedHeadBytes - kPagedPlanBytes, "arrival counts");
 constexpr int kPagedShortSplit = 32, kPagedLongSplit = 16;
 
 struct PagedCall {
@@ -814,20 +817,28 @@ struct PagedCall {
   int page, d, dtype;
 };
 
-// Joins the divided items of the main kernel launched before it, as its
-// programmatic dependent: `ctas` x `shares` blocks, the rows of an item shared.
-template <class E, int D, int ROWS, int TK>
-int paged_merge_launch(const spa::PagedParams& p, int ctas, int shares, cudaStream_t s) {
+// The plan, then the kernel that follows it as its programmatic dependent:
+// that one's set-up overlaps the plan, and it waits for it.
+template <int TK, class K>
+int paged_launch(K kernel, const spa::PagedParams& p, int threads, uint32_t smem, cudaStream_t s,
+                 const CUtensorMap* mq, const CUtensorMap& mk, const CUtensorMap& mv) {
+  spa::spa_paged_plan_kernel<TK><<<1, spa::kPagedPlanThreads, 0, s>>>(p);
+  int st = launch_status();
+  if (st) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)shares, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3((unsigned)p.ctas, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, spa::spa_paged_merge_kernel<E, D, ROWS, TK>, p) != cudaSuccess) return SPA_ERR_CUDA;
+  void* with_q[] = {const_cast<CUtensorMap*>(mq), const_cast<CUtensorMap*>(&mk), const_cast<CUtensorMap*>(&mv),
+                    const_cast<spa::PagedParams*>(&p)};
+  if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), mq ? with_q : with_q + 1) != cudaSuccess)
+    return SPA_ERR_CUDA;
   return launch_status();
 }
 
@@ -843,9 +854,8 @@ int paged_short_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) 
     return st;
   auto* kernel = spa::spa_paged_short_kernel<E, D>;
   if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
-  kernel<<<kPagedShortCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mk, mv, p);
-  if ((st = launch_status())) return st;
-  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedShortCtas, 1, s);
+  p.ctas = kPagedShortCtas;
+  return paged_launch<C::TK>(kernel, p, C::NTHREADS, C::SMEM_BYTES, s, nullptr, mk, mv);
 }
 
 // q [T][Hq][d] viewed as 4-D (d, heads of a group, groups, T): a box holds 64
@@ -878,9 +888,8 @@ int paged_long_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
   auto* kernel = spa::spa_paged_long_kernel<E, D>;
   if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
   if ((st = check_regs(kernel, (int)C::LAUNCH_REGS, regs_ok))) return st;
-  kernel<<<kPagedLongCtas, C::NTHREADS, C::SMEM_BYTES, s>>>(mq, mk, mv, p);
-  if ((st = launch_status())) return st;
-  return paged_merge_launch<E, D, C::ROWS, C::TK>(p, kPagedLongCtas, 64, s);
+  p.ctas = kPagedLongCtas;
+  return paged_launch<C::TK>(kernel, p, C::NTHREADS, C::SMEM_BYTES, s, &mq, mk, mv);
 }
 
 // Groups the query heads into work items of `group` heads (a divisor of the
@@ -1479,7 +1488,7 @@ size_t spa_paged_attn_workspace_bytes(int max_q, int d) {
   if (max_q < 1 || (d != 64 && d != 128)) return 0;
   const int64_t few = 2 * kPagedShortCtas * spa::paged_slot_floats(16, d);
   const int64_t many = 2 * kPagedLongCtas * spa::paged_slot_floats(256, d);
-  return kPagedDescBytes + (size_t)std::max(few, many) * sizeof(float);
+  return kPagedHeadBytes + (size_t)std::max(few, many) * sizeof(float);
 }
 
 int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
@@ -1507,8 +1516,9 @@ int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, cons
   p.q = static_cast<const uint16_t*>(q);
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
-  p.desc = static_cast<int32_t*>(workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedDescBytes);
+  p.plan = static_cast<int4*>(workspace);
+  p.arrived = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + kPagedPlanBytes);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedHeadBytes);
   p.pages = pages;
   p.B = B;
   p.T = T;
@@ -1527,7 +1537,8 @@ int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, cons
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if ((int64_t)p.max_q * (same ? per_kv : 1) <= 16) {
     const int group = same ? per_kv : 1;
-    p.min_run = 2;
+    p.piece_cost = 1;
+    p.min_run = 4;
     p.max_split = kPagedShortSplit;
     if ((st = paged_items(p, bands, group, 16 / group))) return st;
     if (dtype == SPA_BF16)
@@ -1536,7 +1547,8 @@ int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, cons
   }
   int group = 1;
   while (same && group < 128 && per_kv % (2 * group) == 0) group *= 2;
-  p.min_run = 2;
+  p.piece_cost = 2;
+  p.min_run = 4;
   p.max_split = kPagedLongSplit;
   if ((st = paged_items(p, bands, group, 256 / group))) return st;
   if (dtype == SPA_BF16)
