@@ -102,15 +102,17 @@ struct PagedCut {
   int item, off, head, pieces;
 };
 
-constexpr int kPagedPlanThreads = 1024;
+constexpr int kPagedPlanThreads = 512;
 constexpr int kPagedMaxCtas = 296;
 
-// One CTA.  Cuts the line into ctas runs and clears the arrival counts.
+// One CTA.  Cuts the line into ctas runs and clears the arrival counts.  Every
+// thread sums a share of the items; after a scan it knows where its share lies
+// in the line and places the cuts that fall into it.
 template <int TK>
 __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ long long s_sum[32];
-  __shared__ int s_most[32];
-  __shared__ long long s_before[kPagedPlanThreads + 1];  // line before each thread's items
+  constexpr int kWarps = kPagedPlanThreads / 32;
+  __shared__ long long s_sum[kWarps];
+  __shared__ int s_most[kWarps];
   __shared__ int s_item[kPagedMaxCtas + 1], s_off[kPagedMaxCtas + 1];
   // the kernel that follows may be launched: it waits for this one to end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -122,73 +124,78 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
     const int c = paged_item_at<TK>(p, i).cost;
     return c ? c + p.piece_cost : 0;
   };
+  for (int c = threadIdx.x; c < 2 * p.ctas; c += kPagedPlanThreads) p.arrived[c] = 0;
+  for (int c = threadIdx.x; c <= p.ctas; c += kPagedPlanThreads) {
+    s_item[c] = items;
+    s_off[c] = 0;
+  }
   long long mine = 0;
-  int most = 0;
+  int most = 0, only = 0;
   for (int i = i0; i < i1; ++i) {
-    const int c = length(i);
-    mine += c;
-    most = max(most, c);
+    only = length(i);
+    mine += only;
+    most = max(most, only);
   }
   long long incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, m);
     if (lane >= m) incl += v;
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, m));
   }
+  most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 31) s_sum[warp] = incl;
   if (lane == 0) s_most[warp] = most;
-  for (int c = threadIdx.x; c < 2 * p.ctas; c += kPagedPlanThreads) p.arrived[c] = 0;
   __syncthreads();
   long long before = incl - mine, total = 0;
   most = 0;
 #pragma unroll
-  for (int w = 0; w < 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
     most = max(most, s_most[w]);
   }
-  s_before[threadIdx.x] = before;
-  if (threadIdx.x == 0) s_before[kPagedPlanThreads] = total;
-  __syncthreads();
-  long long run = (total + p.ctas - 1) / p.ctas;
+  long long run = total < 2147483647LL - p.ctas ? (long long)(((uint32_t)total + p.ctas - 1) / (uint32_t)p.ctas)
+                                                : (total + p.ctas - 1) / p.ctas;
   run = max(run, (long long)((most + p.max_split - 1) / p.max_split));
   run = max(run, (long long)p.min_run);
-  if ((int)threadIdx.x <= p.ctas) {
-    // the item that holds place run * c of the line, by bisection over the
-    // threads' shares, then within the share
-    const long long at = run * threadIdx.x;
-    int item = items, off = 0;
-    if (at < total) {
-      int a = 0, b = kPagedPlanThreads;  // s_before[a] <= at < s_before[b]
-      while (b - a > 1) {
-        const int m = (a + b) / 2;
-        if (s_before[m] <= at) a = m;
-        else b = m;
+  if (mine > 0) {
+    // the first cut at or behind the share's beginning
+    int c = before + run < 2147483647LL ? (int)(((uint32_t)before + (uint32_t)run - 1) / (uint32_t)run)
+                                        : (int)((before + run - 1) / run);
+    long long at = run * c, x = before;
+    for (int i = i0; i < i1 && at < before + mine; ++i) {
+      const int len = per == 1 ? only : length(i);
+      for (; at < x + len; at += run, ++c) {
+        // a piece of no or one key tile is not worth its beginning: the cut
+        // moves to the item's start or end
+        const int off = (int)(at - x) - p.piece_cost;
+        const bool start = off < 2, end = !start && len - p.piece_cost - off < 2;
+        s_item[c] = end ? i + 1 : i;
+        s_off[c] = start || end ? 0 : off;
       }
-      long long x = s_before[a];
-      item = min(a * per, items);
-      int c = length(item);
-      while (x + c <= at) {
-        x += c;
-        c = length(++item);
-      }
-      // a piece of no or one key tile is not worth its beginning: the cut moves
-      // to the item's start or end
-      off = (int)(at - x) - p.piece_cost;
-      if (off < 2) off = 0;
-      else if (c - p.piece_cost - off < 2) ++item, off = 0;
+      x += len;
     }
-    s_item[threadIdx.x] = item;
-    s_off[threadIdx.x] = off;
   }
   __syncthreads();
   if ((int)threadIdx.x <= p.ctas) {
+    // the cuts within the same item, by bisection: (item, off > 0) never falls
     const int c = threadIdx.x, item = s_item[c], off = s_off[c];
-    int first = c, last = c;  // the cuts within this item
+    int first = c, last = c;
     if (off > 0) {
-      while (first > 0 && s_item[first - 1] == item && s_off[first - 1] > 0) --first;
-      while (last < p.ctas && s_item[last + 1] == item && s_off[last + 1] > 0) ++last;
+      int a = -1;  // the last cut before them
+      for (int hi = c; hi - a > 1;) {
+        const int m = (a + hi) / 2;
+        if (s_item[m] == item && s_off[m] > 0) hi = m;
+        else a = m;
+      }
+      first = a + 1;
+      int b = p.ctas + 1;  // the first cut behind them
+      for (int lo = c; b - lo > 1;) {
+        const int m = (lo + b) / 2;
+        if (s_item[m] == item && s_off[m] > 0) lo = m;
+        else b = m;
+      }
+      last = b - 1;
     }
     p.plan[c] = make_int4(item, off, first - 1, last - first + 2);
   }
@@ -401,6 +408,9 @@ __global__ void __launch_bounds__(160, 2)
     ptx::prefetch_tmap(&tm_v);
   }
   __syncthreads();
+  // The lengths are asked for while the plan is made (they are inputs, written
+  // before it began), so that the walk finds them near.
+  if ((int)threadIdx.x <= p.B) ptx::prefetch_l1(p.cu_q + threadIdx.x), ptx::prefetch_l1(p.kv_len + min((int)threadIdx.x, p.B - 1));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   volatile int* abort_flag = &bars->abort;
   PagedWalk<C::TK> w(p, PagedRun(p));

@@ -233,6 +233,9 @@ __global__ void __launch_bounds__(384, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  // The lengths are asked for while the plan is made (they are inputs, written
+  // before it began), so that the walk finds them near.
+  if ((int)threadIdx.x <= p.B) ptx::prefetch_l1(p.cu_q + threadIdx.x), ptx::prefetch_l1(p.kv_len + min((int)threadIdx.x, p.B - 1));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan
   const uint32_t tmem = bars->tmem_base;
   volatile int* abort_flag = &bars->abort;
