@@ -47,6 +47,7 @@ struct PagedParams {
   int width, page_shift;
   int ctas;           // runs the line is cut into, at most
   int piece_cost;     // cost of a piece besides its key tiles, in key tiles
+  int split_cost;     // what it costs that an item is divided, in key tiles
   int min_run;        // length of a run, at least
   int max_split;      // pieces of an item, about
   float scale_log2;
@@ -107,12 +108,14 @@ constexpr int kPagedMaxCtas = 296;
 
 // One CTA.  Cuts the line into ctas runs and clears the arrival counts.  Every
 // thread sums a share of the items; after a scan it knows where its share lies
-// in the line and places the cuts that fall into it.
+// in the line and places the cuts that fall into it.  Where the longest run of
+// as many whole items as there are per CTA is no longer than an even run and
+// the cost of dividing items, no item is divided.
 template <int TK>
 __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kWarps = kPagedPlanThreads / 32;
   __shared__ long long s_sum[kWarps];
-  __shared__ int s_most[kWarps];
+  __shared__ int s_most[kWarps], s_used[kWarps];
   __shared__ int s_item[kPagedMaxCtas + 1], s_off[kPagedMaxCtas + 1];
   // the kernel that follows may be launched: it waits for this one to end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -130,35 +133,56 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
     s_off[c] = 0;
   }
   long long mine = 0;
-  int most = 0, only = 0;
+  int most = 0, only = 0, used = 0;  // used: items that are not empty
   for (int i = i0; i < i1; ++i) {
     only = length(i);
     mine += only;
     most = max(most, only);
+    used += only > 0;
   }
   long long incl = mine;
+  int incl_used = used;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, m);
-    if (lane >= m) incl += v;
+    const int u = __shfl_up_sync(0xffffffffu, incl_used, m);
+    if (lane >= m) {
+      incl += v;
+      incl_used += u;
+    }
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 31) {
+    s_sum[warp] = incl;
+    s_used[warp] = incl_used;
+  }
   if (lane == 0) s_most[warp] = most;
   __syncthreads();
   long long before = incl - mine, total = 0;
+  int before_used = incl_used - used, all_used = 0;
   most = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_sum[w];
+    if (w < warp) {
+      before += s_sum[w];
+      before_used += s_used[w];
+    }
     total += s_sum[w];
+    all_used += s_used[w];
     most = max(most, s_most[w]);
   }
   long long run = total < 2147483647LL - p.ctas ? (long long)(((uint32_t)total + p.ctas - 1) / (uint32_t)p.ctas)
                                                 : (total + p.ctas - 1) / p.ctas;
   run = max(run, (long long)((most + p.max_split - 1) / p.max_split));
   run = max(run, (long long)p.min_run);
-  if (mine > 0) {
+  const int each = (all_used + p.ctas - 1) / p.ctas;  // whole items per CTA
+  if ((long long)each * most <= run + p.split_cost) {
+    for (int i = i0, u = before_used; used > 0 && i < i1; ++i) {
+      if ((per == 1 ? only : length(i)) == 0) continue;
+      if (u % each == 0) s_item[u / each] = i;
+      ++u;
+    }
+  } else if (mine > 0) {
     // the first cut at or behind the share's beginning
     int c = before + run < 2147483647LL ? (int)(((uint32_t)before + (uint32_t)run - 1) / (uint32_t)run)
                                         : (int)((before + run - 1) / run);
@@ -513,7 +537,10 @@ __global__ void __launch_bounds__(160, 2)
           }
         }
         // masked scores become -inf; base-2 units
-        uint32_t pa[4];
+        // (P in two 16-bit terms, the second the rounding error of the first: one
+        // term alone would add as much error to o as its own rounding, and the
+        // bytes leave time for the second product)
+        uint32_t pa[4], pb[4];
         float alpha[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -535,8 +562,12 @@ __global__ void __launch_bounds__(160, 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) pe[e] = ptx::exp2_approx(v[e] - ref);
           l[x] = fmaf(l[x], alpha[x], (pe[0] + pe[1]) + (pe[2] + pe[3]));
-          pa[x] = E::pack(pe[0], pe[1]);
-          pa[x + 2] = E::pack(pe[2], pe[3]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            pa[x + 2 * e] = E::pack(pe[2 * e], pe[2 * e + 1]);
+            const float2 first = E::unpack(pa[x + 2 * e]);
+            pb[x + 2 * e] = E::pack(pe[2 * e] - first.x, pe[2 * e + 1] - first.y);
+          }
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -565,6 +596,8 @@ __global__ void __launch_bounds__(160, 2)
             ldmatrix_x4_trans(vf, v_base + (chunk / 8) * (C::TK * 128) + ptx::sw128_offset(key, chunk % 8));
             mma_16816<E>(acc[2 * n], pa, vf[0] & keep[0], vf[1] & keep[1]);
             mma_16816<E>(acc[2 * n + 1], pa, vf[2] & keep[0], vf[3] & keep[1]);
+            mma_16816<E>(acc[2 * n], pb, vf[0] & keep[0], vf[1] & keep[1]);
+            mma_16816<E>(acc[2 * n + 1], pb, vf[2] & keep[0], vf[3] & keep[1]);
           }
         }
       }

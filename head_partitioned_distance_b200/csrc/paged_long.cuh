@@ -581,13 +581,13 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t pk[16];
+          if (q == 3 && pass_turn) ptx::mbar_arrive(&bars->turn[1 - t]);  // the other may start up
           paged_exp32<E>(s[q], c2v, mnv, sa, sb, pk);
           if (q == 2) {  // the first half has been stored meanwhile
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&bars->p_full[t][0]);
           }
-          if (q == 3 && pass_turn) ptx::mbar_arrive(&bars->turn[1 - t]);
           ptx::tmem_st16(tS + q * 16, pk);
         }
         ptx::tmem_wait_st();
