@@ -33,7 +33,7 @@ struct PagedParams {
   const uint16_t* q;  // [T][Hq][d]
   uint16_t* o;        // [T][Hq][d]
   float* lse;         // [T][Hq]
-  int4* plan;         // PagedCut of every CTA and of the end
+  int4* plan;         // PagedCut of every CTA and of the end; null: CTA i has item i
   int32_t* arrived;   // pieces that have left their partial, by the CTA that began the item (x 2 row halves)
   float* part;        // two partial slots per CTA
   int64_t pages;
@@ -229,6 +229,11 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
 struct PagedRun {
   PagedCut from, to;
   __device__ __forceinline__ explicit PagedRun(const PagedParams& p) {
+    if (!p.plan) {  // one whole item per CTA
+      from = {(int)blockIdx.x, 0, 0, 0};
+      to = {(int)blockIdx.x + 1, 0, 0, 0};
+      return;
+    }
     const int4 a = p.plan[blockIdx.x], b = p.plan[blockIdx.x + 1];
     from = {a.x, a.y, a.z, a.w};
     to = {b.x, b.y, b.z, b.w};

@@ -810,6 +810,8 @@ static_assert(kPagedShortCtas <= spa::kPagedMaxCtas && kPagedLongCtas <= spa::kP
 static_assert((spa::kPagedMaxCtas + 1) * sizeof(int4) <= kPagedPlanBytes, "cuts");
 static_assert(2 * spa::kPagedMaxCtas * sizeof(int32_t) <= kPagedHeadBytes - kPagedPlanBytes, "arrival counts");
 constexpr int kPagedShortSplit = 32, kPagedLongSplit = 16;
+// key tiles up to which an item is left whole without a plan
+constexpr int kPagedShortWhole = 10, kPagedLongWhole = 12;
 
 struct PagedCall {
   const void* k_pages;
@@ -817,14 +819,37 @@ struct PagedCall {
   int page, d, dtype;
 };
 
+// Key tiles that an item can have at most, whatever the lengths.
+template <int TK>
+int64_t paged_most_tiles(const spa::PagedParams& p) {
+  int64_t span = 0;
+  for (int g = 0; g < p.ng; ++g) span = std::max(span, (int64_t)p.hi[g] - p.lo[g]);
+  span = std::min(span + std::min(p.blk_tokens, p.max_q) - 1, (int64_t)p.width << p.page_shift);
+  return (span + TK - 2) / TK + 1;
+}
+
 // The plan, then the kernel that follows it as its programmatic dependent:
-// that one's set-up overlaps the plan, and it waits for it.
+// that one's set-up overlaps the plan, and it waits for it.  Without a plan CTA
+// i has item i: where there are no more items than CTAs and none can be longer
+// than `whole` key tiles, or twice that when the items take more than half of
+// the CTAs, so that dividing them could not gain what the plan costs.  Measured
+// (plan / no plan): 8 items of at most 9 tiles of 64 keys 13.2 / 10.3 us, of 17
+// tiles 14.0 / 17.3; 64 items of 17 tiles 16.7 / 18.6, 256 items of 17 tiles
+// 26.4 / 23.2; 8 items of at most 9 tiles of 128 keys 24.5 / 22.4, of 17 tiles
+// 30.3 / 37.2.
 template <int TK, class K>
-int paged_launch(K kernel, const spa::PagedParams& p, int threads, uint32_t smem, cudaStream_t s,
+int paged_launch(K kernel, spa::PagedParams& p, int ctas, int whole, int threads, uint32_t smem, cudaStream_t s,
                  const CUtensorMap* mq, const CUtensorMap& mk, const CUtensorMap& mv) {
-  spa::spa_paged_plan_kernel<TK><<<1, spa::kPagedPlanThreads, 0, s>>>(p);
-  int st = launch_status();
-  if (st) return st;
+  int st;
+  const int64_t items = (int64_t)p.B * p.ng * p.nblk;
+  const bool planned = items > ctas || paged_most_tiles<TK>(p) > (2 * items > ctas ? 2 * whole : whole);
+  p.ctas = planned ? ctas : (int)items;
+  if (planned) {
+    spa::spa_paged_plan_kernel<TK><<<1, spa::kPagedPlanThreads, 0, s>>>(p);
+    if ((st = launch_status())) return st;
+  } else {
+    p.plan = nullptr;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas, 1, 1);
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -834,7 +859,7 @@ int paged_launch(K kernel, const spa::PagedParams& p, int threads, uint32_t smem
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = planned ? 1 : 0;
   void* with_q[] = {const_cast<CUtensorMap*>(mq), const_cast<CUtensorMap*>(&mk), const_cast<CUtensorMap*>(&mv),
                     const_cast<spa::PagedParams*>(&p)};
   if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), mq ? with_q : with_q + 1) != cudaSuccess)
@@ -854,8 +879,7 @@ int paged_short_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) 
     return st;
   auto* kernel = spa::spa_paged_short_kernel<E, D>;
   if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
-  p.ctas = kPagedShortCtas;
-  return paged_launch<C::TK>(kernel, p, C::NTHREADS, C::SMEM_BYTES, s, nullptr, mk, mv);
+  return paged_launch<C::TK>(kernel, p, kPagedShortCtas, kPagedShortWhole, C::NTHREADS, C::SMEM_BYTES, s, nullptr, mk, mv);
 }
 
 // q [T][Hq][d] viewed as 4-D (d, heads of a group, groups, T): a box holds 64
@@ -888,8 +912,7 @@ int paged_long_launch(const PagedCall& c, spa::PagedParams& p, cudaStream_t s) {
   auto* kernel = spa::spa_paged_long_kernel<E, D>;
   if ((st = prepare_kernel(kernel, C::SMEM_BYTES, prepared))) return st;
   if ((st = check_regs(kernel, (int)C::LAUNCH_REGS, regs_ok))) return st;
-  p.ctas = kPagedLongCtas;
-  return paged_launch<C::TK>(kernel, p, C::NTHREADS, C::SMEM_BYTES, s, &mq, mk, mv);
+  return paged_launch<C::TK>(kernel, p, kPagedLongCtas, kPagedLongWhole, C::NTHREADS, C::SMEM_BYTES, s, &mq, mk, mv);
 }
 
 // Groups the query heads into work items of `group` heads (a divisor of the

@@ -9,6 +9,7 @@ library reports an error.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -78,7 +79,7 @@ EXPORTS = {
     "spa_paged_append": ([_vp] * 12 + [_int, _int, _int, _int, _int, _i64, _int, _int, _int, _i64, _i64p, _i64p, _i64p,
                                        _int, _f32, _int, _vp], _int),
     "spa_paged_attn_workspace_bytes": ([_int, _int], ctypes.c_size_t),
-    "spa_paged_attn": ([_vp] * 9 + [_int, _int, _int, _int, _int, _i64, _int, _int, _i64, _int, _f32, _i32p, _i32p,
+    "spa_paged_attn": ([_vp] * 9 + [_int, _int, _int, _int, _int, _i64, _int, _int, _i64, _int, _f32, _vp, _vp,
                                     _int, _vp], _int),
 }
 for _name, (_args, _res) in EXPORTS.items():
@@ -673,30 +674,32 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
 
 def _need_on(t, shape, dtype, device, name):
     """A contiguous tensor of this shape and type on `device`."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _vector_rows(t) -> bool:
     """Rows (the last dimension) contiguous and every row 16-byte aligned."""
-    *outer, last = t.stride()
-    if last != 1 or t.data_ptr() % 16:
+    if t.data_ptr() % 16:
         return False
-    for n, s in zip(t.shape, outer):
-        if s % 8 and n != 1:
-            return False
-    return True
+    if t.is_contiguous() and t.shape[-1] % 8 == 0:
+        return True
+    *outer, last = t.stride()
+    return last == 1 and all(s % 8 == 0 or n == 1 for n, s in zip(t.shape, outer))
 
 
 def _need_rows(t, shape, dtype, device, name):
-    """A tensor of this shape and type on `device`, its rows readable in 16-byte vectors."""
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    """A tensor of this shape and type on `device`, its rows readable in 16-byte
+    vectors; returns its address and its strides for a C entry point."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not _vector_rows(t):
         raise ValueError(f"{name}: the last dimension must be contiguous, rows 16-byte aligned and the other strides "
                          f"multiples of 8, got strides {t.stride()}")
+    return t.data_ptr(), _strides(t)
 
 
 _Strides2, _Strides3 = _i64 * 2, _i64 * 3
@@ -752,17 +755,16 @@ def spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, q_out, k_out, position
     """q_out, k_out = the normed and rotated q [B, Hq, N, d], k [B, Hk, N, d]
     (bf16 or fp16, any strides of whole 16-byte vectors); see spa.h."""
     B, Hq, Hk, N, d = _qk_dims(q, k)
-    dt, dev = _dtype_code(q, "q"), q.device
-    _need_rows(q, (B, Hq, N, d), q.dtype, dev, "q")
-    _need_rows(k, (B, Hk, N, d), q.dtype, dev, "k")
-    _need_on(q_out, (B, Hq, N, d), q.dtype, dev, "q_out")
-    _need_on(k_out, (B, Hk, N, d), q.dtype, dev, "k_out")
-    _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
-    _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
+    dt, ty, dev = _dtype_code(q, "q"), q.dtype, q.device
+    q_shape, k_shape = (B, Hq, N, d), (B, Hk, N, d)
+    pq, sq = _need_rows(q, q_shape, ty, dev, "q")
+    pk, sk = _need_rows(k, k_shape, ty, dev, "k")
+    pqo, pko = _need_on(q_out, q_shape, ty, dev, "q_out"), _need_on(k_out, k_shape, ty, dev, "k_out")
+    pqw = _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
+    pkw = _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
     rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
-    _launch(dev, "spa_qk_norm_rope_fwd", _lib.spa_qk_norm_rope_fwd, q.data_ptr(), k.data_ptr(), q_weight.data_ptr(),
-            k_weight.data_ptr(), table.data_ptr(), pos, q_out.data_ptr(), k_out.data_ptr(), B, Hq, Hk, N, d, rot,
-            table.shape[0], pos_stride, _strides(q), _strides(k), int(interleaved), eps, dt, _stream_on(dev, stream))
+    _launch(dev, "spa_qk_norm_rope_fwd", _lib.spa_qk_norm_rope_fwd, pq, pk, pqw, pkw, table.data_ptr(), pos, pqo, pko,
+            B, Hq, Hk, N, d, rot, table.shape[0], pos_stride, sq, sk, interleaved, eps, dt, _stream_on(dev, stream))
     return q_out, k_out
 
 
@@ -777,21 +779,19 @@ def spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk
     workspace: CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes."""
     B, Hq, Hk, N, d = _qk_dims(q, k)
     dt, dev = _dtype_code(q, "q"), q.device
-    for t, H, n in ((q, Hq, "q"), (k, Hk, "k"), (dq, Hq, "dq"), (dk, Hk, "dk")):
-        _need_rows(t, (B, H, N, d), q.dtype, dev, n)
-    _need_on(dq_out, (B, Hq, N, d), q.dtype, dev, "dq_out")
-    _need_on(dk_out, (B, Hk, N, d), q.dtype, dev, "dk_out")
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-        _need_on(t, (d,), torch.float32, dev, n)
+    ty, q_shape, k_shape = q.dtype, (B, Hq, N, d), (B, Hk, N, d)
+    (pq, sq), (pk, sk) = _need_rows(q, q_shape, ty, dev, "q"), _need_rows(k, k_shape, ty, dev, "k")
+    (pdq, sdq), (pdk, sdk) = _need_rows(dq, q_shape, ty, dev, "dq"), _need_rows(dk, k_shape, ty, dev, "dk")
+    pdqo, pdko = _need_on(dq_out, q_shape, ty, dev, "dq_out"), _need_on(dk_out, k_shape, ty, dev, "dk_out")
+    pqw, pkw, pdqw, pdkw = (_need_on(t, (d,), torch.float32, dev, n) for t, n in (
+        (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight")))
     if workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < spa_qk_norm_rope_bwd_workspace_bytes(d):
         raise ValueError("workspace: contiguous CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes")
     rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
-    _launch(dev, "spa_qk_norm_rope_bwd", _lib.spa_qk_norm_rope_bwd, dq_out.data_ptr(), dk_out.data_ptr(),
-            q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), pos,
-            dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), B, Hq, Hk,
-            N, d, rot, table.shape[0], pos_stride, _strides(q), _strides(k), _strides(dq), _strides(dk),
-            int(interleaved), eps, dt, _stream_on(dev, stream))
+    _launch(dev, "spa_qk_norm_rope_bwd", _lib.spa_qk_norm_rope_bwd, pdqo, pdko, pq, pk, pqw, pkw, table.data_ptr(), pos,
+            pdq, pdk, pdqw, pdkw, workspace.data_ptr(), B, Hq, Hk, N, d, rot, table.shape[0], pos_stride, sq, sk, sdq,
+            sdk, interleaved, eps, dt, _stream_on(dev, stream))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -852,17 +852,16 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps: float = 1
 
 # ------------------------------------------------------------- paged cache
 def _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, dtype, device):
-    """Checks the cache's tensors; returns (B, pages, page, width)."""
+    """Checks the cache's tensors; returns (B, pages, page, width, their addresses)."""
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("k_pages and v_pages are [pages, Hk, page, d], page_table is [B, width]")
     pages, page = k_pages.shape[0], k_pages.shape[2]
     B, width = page_table.shape
-    _need_on(k_pages, (pages, Hk, page, d), dtype, device, "k_pages")
-    _need_on(v_pages, (pages, Hk, page, d), dtype, device, "v_pages")
-    _need_on(page_table, (B, width), torch.int32, device, "page_table")
-    _need_on(cu_q, (B + 1,), torch.int32, device, "cu_q")
-    _need_on(kv_len, (B,), torch.int32, device, "kv_len")
-    return B, pages, page, width
+    shape = (pages, Hk, page, d)
+    ptrs = (_need_on(k_pages, shape, dtype, device, "k_pages"), _need_on(v_pages, shape, dtype, device, "v_pages"),
+            _need_on(page_table, (B, width), torch.int32, device, "page_table"),
+            _need_on(cu_q, (B + 1,), torch.int32, device, "cu_q"), _need_on(kv_len, (B,), torch.int32, device, "kv_len"))
+    return B, pages, page, width, ptrs
 
 
 def spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, q_out, k_pages, v_pages,
@@ -873,19 +872,18 @@ def spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_tabl
         raise ValueError("q, k and v are [T, H, d]")
     T, Hq, d = q.shape
     Hk = k.shape[1]
-    dt, dev = _dtype_code(q, "q"), q.device
-    _need_rows(q, (T, Hq, d), q.dtype, dev, "q")
-    _need_rows(k, (T, Hk, d), q.dtype, dev, "k")
-    _need_rows(v, (T, Hk, d), q.dtype, dev, "v")
-    _need_on(q_out, (T, Hq, d), q.dtype, dev, "q_out")
-    _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
-    _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
-    B, pages, page, width = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, q.dtype, dev)
+    dt, ty, dev = _dtype_code(q, "q"), q.dtype, q.device
+    pq, sq = _need_rows(q, (T, Hq, d), ty, dev, "q")
+    pk, sk = _need_rows(k, (T, Hk, d), ty, dev, "k")
+    pv, sv = _need_rows(v, (T, Hk, d), ty, dev, "v")
+    po = _need_on(q_out, (T, Hq, d), ty, dev, "q_out")
+    pqw = _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
+    pkw = _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
+    B, pages, page, width, (pkp, pvp, ppt, pcu, pkv) = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d,
+                                                                  ty, dev)
     rot, _, _ = _rope_args(table, None, 1, 0, dev)
-    _launch(dev, "spa_paged_append", _lib.spa_paged_append, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            q_weight.data_ptr(), k_weight.data_ptr(), table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(),
-            page_table.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), B, T, Hq, Hk, d, pages,
-            page, width, rot, table.shape[0], _strides(q), _strides(k), _strides(v), int(interleaved), eps, dt,
+    _launch(dev, "spa_paged_append", _lib.spa_paged_append, pq, pk, pv, pqw, pkw, table.data_ptr(), pcu, pkv, ppt, po,
+            pkp, pvp, B, T, Hq, Hk, d, pages, page, width, rot, table.shape[0], sq, sk, sv, interleaved, eps, dt,
             _stream_on(dev, stream))
     return q_out
 
@@ -913,22 +911,20 @@ def spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, o,
         raise ValueError("q is [T, Hq, d], k_pages and v_pages are [pages, Hk, page, d]")
     T, Hq, d = q.shape
     Hk = k_pages.shape[1]
-    dt, dev = _dtype_code(q, "q"), q.device
-    _need_on(q, (T, Hq, d), q.dtype, dev, "q")
-    _need_on(o, (T, Hq, d), q.dtype, dev, "o")
-    _need_on(lse, (T, Hq), torch.float32, dev, "lse")
-    B, pages, page, width = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, q.dtype, dev)
+    dt, ty, dev = _dtype_code(q, "q"), q.dtype, q.device
+    pq, po = _need_on(q, (T, Hq, d), ty, dev, "q"), _need_on(o, (T, Hq, d), ty, dev, "o")
+    pl = _need_on(lse, (T, Hq), torch.float32, dev, "lse")
+    B, pages, page, width, (pkp, pvp, ppt, pcu, pkv) = _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d,
+                                                                  ty, dev)
     if workspace.device != dev or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < spa_paged_attn_workspace_bytes(max_q, d):
         raise ValueError("workspace: contiguous CUDA tensor of spa_paged_attn_workspace_bytes(max_q, d) bytes")
     if (lo is not None and len(lo) != Hq) or (hi is not None and len(hi) != Hq):
         raise ValueError(f"lo and hi: {Hq} entries, one for each query head")
-    lo_a = None if lo is None else _i32(lo)
-    hi_a = None if hi is None else _i32(hi)
-    _launch(dev, "spa_paged_attn", _lib.spa_paged_attn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), o.data_ptr(), lse.data_ptr(),
-            workspace.data_ptr(), B, T, max_q, Hq, Hk, pages, page, width, N, d, scale, lo_a, hi_a, dt,
-            _stream_on(dev, stream))
+    lo_a, hi_a = (None if x is None else array.array("i", x) for x in (lo, hi))
+    _launch(dev, "spa_paged_attn", _lib.spa_paged_attn, pq, pkp, pvp, ppt, pcu, pkv, po, pl, workspace.data_ptr(), B, T,
+            max_q, Hq, Hk, pages, page, width, N, d, scale, lo_a and lo_a.buffer_info()[0],
+            hi_a and hi_a.buffer_info()[0], dt, _stream_on(dev, stream))
     return o, lse
 
 
