@@ -10,8 +10,8 @@ fp16, 2^-25).  Before that it is formed in fp32 with unit roundoff u = 2^-24:
                                       -> 16 u < 1e-6 of |a c| + |b s|
   dx     g: 3 u; the row's dot product: 16 u of sum |g w x|; its factors: 24 u
          -> less than 60 u < 4e-6 of r (|g w| + |x| r^2 mean|g w x|)
-  dw     every term 20 u; summed along at most 64 rows of a lane, 32 lane
-         groups, 19 partials and 5 shuffles: 120 u -> 140 u < 1e-5 of sum |g n|
+  dw     every term 20 u; summed along at most 64 rows of a lane, 16 lane
+         groups, 28 partials and 5 shuffles: 113 u -> 140 u < 1e-5 of sum |g n|
 """
 import math
 
@@ -284,6 +284,28 @@ def test_other_stream_and_graph(spa):
     graph.replay()
     for a, b in zip(fwd + bwd, spa.qk_norm_rope_forward(q, k, wq, wk, table)
                     + spa.qk_norm_rope_backward(dq, dk, q, k, wq, wk, table)):
+        assert torch.equal(a, b)
+
+
+def test_forward_and_backward_in_one_graph(spa):
+    # a training step's part, captured: autograd inside the capture
+    q, k, wq, wk = make(1, 4, 2, 100, 64, torch.bfloat16, 3)
+    table = spa.rope_table(100, 64)
+    leaves = [t.detach().clone().requires_grad_() for t in (q, k, wq, wk)]
+    dq, dk = torch.randn(1, 4, 100, 64, device=DEV).bfloat16(), torch.randn(1, 2, 100, 64, device=DEV).bfloat16()
+    step = lambda: torch.autograd.grad(spa.qk_norm_rope(*leaves, table), leaves, (dq, dk))  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    with torch.no_grad():
+        leaves[0].copy_(torch.randn_like(q))
+    graph.replay()
+    for a, b in zip(got, step()):
         assert torch.equal(a, b)
 
 

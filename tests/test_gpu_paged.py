@@ -178,11 +178,40 @@ def test_many_rows(spa, seqs, page, Hq, Hk, d, dtype, kind):
     assert spa.spa_device_status() == spa.SPA_OK
 
 
-# long sequences: items cut over many CTAs, joined by the merge
+# more items than CTAs: the plan cuts the line of all items (with and without
+# dividing one), over empty sequences, sequences without keys and single rows
+def _crowd(n, most, seed, rows):
+    g = torch.Generator().manual_seed(seed)
+    seqs = []
+    for i in range(n):
+        new = 0 if i % 11 == 5 else int(torch.randint(1, rows + 1, (1,), generator=g))
+        seqs.append((new, new + int(torch.randint(0, most, (1,), generator=g)) if i % 7 else new // 2))
+    return seqs
+
+
+@pytest.mark.parametrize("seqs,page,Hq,Hk,d,dtype,kind", [
+    (_crowd(170, 200, 1, 1), 16, 4, 4, 64, BF, "balanced"),
+    (_crowd(90, 900, 2, 4), 32, 8, 2, 128, FP, "full"),
+    ([(1, 4000)] + _crowd(80, 60, 3, 1), 64, 4, 4, 64, BF, "full"),
+    (_crowd(60, 150, 4, 150), 16, 4, 2, 64, FP, "window70"),
+    (_crowd(40, 500, 5, 60), 64, 4, 4, 128, BF, "balanced"),
+    ([(300, 3000)] + _crowd(50, 40, 6, 30), 32, 4, 1, 128, BF, "full"),
+])
+def test_more_items_than_ctas(spa, seqs, page, Hq, Hk, d, dtype, kind):
+    c = Case(seqs, page, Hq, Hk, d, dtype, kind, seed=len(seqs))
+    o, lse = c.run(spa)
+    c.check(o, lse)
+    again = c.run(spa)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+    assert spa.spa_device_status() == spa.SPA_OK
+
+
+# long sequences: items cut over many CTAs, their pieces joined by the last to arrive
 @pytest.mark.parametrize("seqs,Hq,Hk,d,dtype,kind", [
     ([(1, 30001)], 4, 1, 128, BF, "full"), ([(1, 9000), (1, 50), (1, 4000)], 8, 8, 64, BF, "full"),
     ([(3, 20000)], 2, 1, 64, FP, "far100"), ([(20, 12000), (1, 100)], 4, 1, 128, BF, "full"),
-    ([(200, 9000)], 2, 2, 64, FP, "window5000"),
+    ([(200, 9000)], 2, 2, 64, FP, "window5000"), ([(1, 150001)], 1, 1, 64, BF, "full"),
+    ([(2, 40000), (1, 39000)], 3, 3, 64, FP, "balanced"), ([(300, 20000), (130, 17000)], 2, 1, 128, BF, "far15000"),
 ])
 def test_split_rows(spa, seqs, Hq, Hk, d, dtype, kind):
     c = Case(seqs, 64, Hq, Hk, d, dtype, kind, seed=3)
@@ -302,6 +331,39 @@ def test_two_streams_at_once(spa):
     for w, outs in zip(want, got):
         for o, lse in outs:
             assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_offsets_past_32_bits(spa, new):
+    # the last pages of a cache of 2^31 + elements, written and read
+    pages, page, Hk, d, n = 33000, 128, 4, 128, 200
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    kp = torch.empty(pages, Hk, page, d, dtype=BF, device=DEV)
+    vp = torch.empty(pages, Hk, page, d, dtype=BF, device=DEV)
+    assert kp.numel() > 2 ** 31
+    small = [torch.empty(2, Hk, page, d, dtype=BF, device=DEV) for _ in range(2)]
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn(n, 3 * Hk, d, generator=g).to(BF).to(DEV)
+    w, rope = torch.ones(d, device=DEV), spa.rope_table(n, d)
+    outs = []
+    for k_pages, v_pages, table in ((kp, vp, [pages - 1, pages - 2]), (*small, [0, 1])):
+        table, kv = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([table], [n]))
+        cu = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        q = spa.paged_append(*qkv.split(Hk, 1), k_pages, v_pages, table, cu, kv, w, w, rope)
+        cu = torch.tensor([0, new], dtype=torch.int32, device=DEV)
+        outs.append(spa.paged_attention(q[-new:].contiguous(), k_pages, v_pages, table, cu, kv, new, lo=[0] * Hk,
+                                        hi=[n] * Hk, N=n))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert spa.spa_device_status() == spa.SPA_OK and not outs[0][0].isnan().any()
+
+
+def test_sequences_may_share_pages(spa):
+    # a common prefix, read by two sequences through the same pages
+    c = Case([(1, 64), (1, 64)], 16, 4, 2, 64, BF, "full", seed=2)
+    c.table[1, :4] = c.table[0, :4]
+    c.k[1], c.v[1] = c.k[0], c.v[0]
+    c.check(*c.run(spa))
 
 
 def test_no_rows(spa):
