@@ -1,5 +1,5 @@
 // paged_long.cuh -- attention of many new tokens per sequence over a paged
-// cache (the work list, the mask and the merge are in paged.cuh).
+// cache (the work list and the mask are in paged.cuh).
 //
 // The pipeline of the training forward (fwd.cuh) over the paged work list:
 // one CTA per SM, an item is up to 256 rows of one head group, two Q tiles of
@@ -18,8 +18,16 @@
 // outside the range (0 times no number is no number).  Scores of such keys are
 // replaced, not added to, by the mask.
 //
-// Bound by the exponentials and the tensor core (a 128 x 128 tile takes 1024
-// cycles of the 16 special-function lanes and 512 of the tensor core).
+// Bound by the chain of one Q tile's step, S -> P -> O -> next S: 770 cycles to
+// fetch the scores and find their max, 1440 for the exponentials (1024 of the
+// special-function lanes), 1350 for the two products (2 x 512 of the tensor
+// core, and the signals between them), against which the other tile's step is
+// set.  4096 tokens of 32 heads over 16384 positions of one key/value head:
+// 1240 TFLOP/s, 75 % of the measured bf16 rate.  Tried and slower there: 64-key
+// tiles with S ahead of the softmax (the issuing thread's own instructions
+// then take longer than the products: 970), a polynomial for part of the
+// exponentials (more instructions than it saves lanes: 1130 at a quarter), the
+// max beside the exponentials (spills: 1160).
 #pragma once
 
 #include "paged.cuh"
@@ -28,8 +36,8 @@ namespace spa {
 
 // K and V have rings of their own: a K stage is free as soon as both tiles'
 // S are done, a V stage after both tiles' O products, so that each is asked
-// for about two steps before it is used.  (With one ring for both, released
-// after the O products, a step of keys from DRAM took 3.5 us instead of XX.)
+// for about two steps before it is used (one ring for both, released after the
+// O products, took 10 % longer over 16384 positions).
 template <int D>
 struct PagedLongCfg {
   static constexpr int ROWS = 256, TK = 128;

@@ -571,8 +571,8 @@ SPA_API int spa_paged_append(const void* q, const void* k, const void* v, const 
  * rows attend to and others do not must be finite.  A page number outside
  * [0, pages) that is needed, or a kv_len beyond the page table, counts as keys
  * of zeros there or as no keys, and spa_device_status reports SPA_ERR_INVAL.
- * Lengths are read on the device only: a captured call follows them.  Two
- * launches; results are the same from call to call.  T = 0 launches nothing.
+ * Lengths are read on the device only: a captured call follows them.  One or
+ * two launches; results are the same from call to call.  T = 0 launches nothing.
  * SPA_ERR_INVAL for null pointers, sizes < 1, Hq not a multiple of Hk, bad
  * bands, a scale that is not finite and > 0 or an unknown dtype;
  * SPA_ERR_UNSUPPORTED for d not in {64, 128}, Hq > 256, B > 65535, a page size
