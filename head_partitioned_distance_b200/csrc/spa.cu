@@ -679,6 +679,11 @@ bool vector_strides(const int64_t* s, int64_t B, int64_t H, int64_t N) {
   return (B == 1 || s[0] % 8 == 0) && (H == 1 || s[1] % 8 == 0) && (N == 1 || s[2] % 8 == 0);
 }
 
+// Rows that are written do not lie on top of one another.
+bool apart_strides(const int64_t* s, int64_t B, int64_t H, int64_t N) {
+  return (B == 1 || s[0] != 0) && (H == 1 || s[1] != 0) && (N == 1 || s[2] != 0);
+}
+
 spa::RowStrides row_strides(const int64_t* s) { return {s[0], s[1], s[2]}; }
 
 int check_norm_rope(int64_t heads, int d, int rot, int64_t table_len, float eps, int dtype) {
@@ -1417,6 +1422,7 @@ int spa_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, 
       (st = check_norm_rope((int64_t)Hq + Hk, d, rot, table_len, eps, dtype)))
     return st;
   if (!positions && N > table_len) return SPA_ERR_INVAL;
+  if (!apart_strides(dq_strides, B, Hq, N) || !apart_strides(dk_strides, B, Hk, N)) return SPA_ERR_INVAL;
   for (const void* t : {dq_out, dk_out, q, k, (const void*)wq, (const void*)wk, (const void*)table, (const void*)dq,
                         (const void*)dk, (const void*)workspace})
     if (!aligned(t, 16)) return SPA_ERR_UNSUPPORTED;

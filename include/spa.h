@@ -483,7 +483,8 @@ SPA_API int spa_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, 
  *   dw = sum over rows and heads of g * n,   dx = r (g * w - n mean(g * w * n)).
  *   dq_out, dk_out: gradients of q_out, k_out, contiguous as those
  *   dq, dk:         outputs, written through dq_strides, dk_strides (rules of
- *                   the inputs' strides; no two elements may share memory)
+ *                   the inputs' strides, and none 0 where its extent is
+ *                   above one: no two elements may share memory)
  *   dwq, dwk:       outputs, fp32 [d]
  *   workspace:      DEVICE buffer of spa_qk_norm_rope_bwd_workspace_bytes(d)
  *                   bytes, 16-byte aligned, caller-owned, overwritten
@@ -534,7 +535,7 @@ SPA_API int spa_rope_table(float* table, int64_t length, int rot, double base, v
  * A token whose position lies outside the table or the page table's width, or
  * whose page number lies outside [0, pages), gets a zero q_out row and no
  * place in the cache, and spa_device_status reports SPA_ERR_INVAL.  Two tokens
- * must not share a place.  One launch; T = 0 launches nothing.  Errors as
+ * must not share a place, and no output may overlap an input.  One launch; T = 0 launches nothing.  Errors as
  * spa_qk_norm_rope_fwd, and SPA_ERR_UNSUPPORTED for a page size outside the
  * rule above, Hq + 2 Hk > 1024 or B > 65535.
  */

@@ -65,6 +65,7 @@ def test_backward_refuses():
         p[i] = ODD
         assert bwd(p) == spa.SPA_ERR_UNSUPPORTED
     assert bwd(dqs=(25600, 6400, 63)) == spa.SPA_ERR_UNSUPPORTED
+    assert bwd(dqs=(25600, 0, 64)) == spa.SPA_ERR_INVAL  # heads of a gradient on top of one another
     assert bwd(d=32) == spa.SPA_ERR_UNSUPPORTED
     assert bwd(length=50) == spa.SPA_ERR_INVAL
     assert spa.spa_qk_norm_rope_bwd_workspace_bytes(96) == 0
