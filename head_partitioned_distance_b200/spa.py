@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import functools
 import os
 
 import torch
@@ -737,7 +738,8 @@ def _qk_dims(q, k):
 def spa_rope_table(table, base: float, stream=None):
     """Fill table [length, rot / 2, 2] fp32 with (cos, sin) of pos * base^(-2 i / rot)."""
     if table.dim() != 3 or table.shape[2] != 2 or not table.is_cuda:
-        raise ValueError(f"table: expected CUDA tensor [length, rot / 2, 2], got {tuple(table.shape)} on {table.device}")
+        raise ValueError(f"table: expected CUDA tensor [length, rot / 2, 2], got {tuple(table.shape)} on "
+                         f"{table.device}")
     _need_on(table, table.shape, torch.float32, table.device, "table")
     _launch(table.device, "spa_rope_table", _lib.spa_rope_table, table.data_ptr(), table.shape[0], 2 * table.shape[1],
             base, _stream_on(table.device, stream))
@@ -768,6 +770,7 @@ def spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, q_out, k_out, position
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=None)
 def spa_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
     return int(_lib.spa_qk_norm_rope_bwd_workspace_bytes(d))
 
@@ -860,7 +863,8 @@ def _need_cache(k_pages, v_pages, page_table, cu_q, kv_len, Hk, d, dtype, device
     shape = (pages, Hk, page, d)
     ptrs = (_need_on(k_pages, shape, dtype, device, "k_pages"), _need_on(v_pages, shape, dtype, device, "v_pages"),
             _need_on(page_table, (B, width), torch.int32, device, "page_table"),
-            _need_on(cu_q, (B + 1,), torch.int32, device, "cu_q"), _need_on(kv_len, (B,), torch.int32, device, "kv_len"))
+            _need_on(cu_q, (B + 1,), torch.int32, device, "cu_q"),
+            _need_on(kv_len, (B,), torch.int32, device, "kv_len"))
     return B, pages, page, width, ptrs
 
 
@@ -898,6 +902,7 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q_weight, 
                             interleaved)
 
 
+@functools.lru_cache(maxsize=64)
 def spa_paged_attn_workspace_bytes(max_q: int, d: int) -> int:
     return int(_lib.spa_paged_attn_workspace_bytes(max_q, d))
 
