@@ -681,14 +681,17 @@ def _need_on(t, shape, dtype, device, name):
     return t.data_ptr()
 
 
-def _vector_rows(t) -> bool:
+def _vector_rows(t, strides) -> bool:
     """Rows (the last dimension) contiguous and every row 16-byte aligned."""
-    if t.data_ptr() % 16:
+    if strides[-1] != 1 or t.data_ptr() % 16:
         return False
-    if t.is_contiguous() and t.shape[-1] % 8 == 0:
-        return True
-    *outer, last = t.stride()
-    return last == 1 and all(s % 8 == 0 or n == 1 for n, s in zip(t.shape, outer))
+    for n, s in zip(t.shape, strides[:-1]):
+        if s % 8 and n != 1:
+            return False
+    return True
+
+
+_Strides2, _Strides3 = _i64 * 2, _i64 * 3
 
 
 def _need_rows(t, shape, dtype, device, name):
@@ -697,18 +700,11 @@ def _need_rows(t, shape, dtype, device, name):
     if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name}: expected {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    if not _vector_rows(t):
+    strides = t.stride()
+    if not _vector_rows(t, strides):
         raise ValueError(f"{name}: the last dimension must be contiguous, rows 16-byte aligned and the other strides "
-                         f"multiples of 8, got strides {t.stride()}")
-    return t.data_ptr(), _strides(t)
-
-
-_Strides2, _Strides3 = _i64 * 2, _i64 * 3
-
-
-def _strides(t):
-    s = t.stride()
-    return _Strides3(*s[:3]) if len(s) == 4 else _Strides2(*s[:2])
+                         f"multiples of 8, got strides {strides}")
+    return t.data_ptr(), _Strides3(*strides[:3]) if len(strides) == 4 else _Strides2(*strides[:2])
 
 
 def _rope_args(table, positions, B, N, device):
@@ -806,22 +802,15 @@ def qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions=None, eps: f
     return spa_qk_norm_rope_fwd(q, k, q_weight, k_weight, table, qo, ko, positions, eps, interleaved)
 
 
-def _grad_like(x):
-    """An empty gradient of x [B, H, N, d], dense and in x's order of heads and rows."""
-    B, H, N, d = x.shape
-    _, sh, sn, _ = x.stride()
-    strides = (N * H * d, d, H * d, 1) if sh < sn else (H * N * d, N * d, d, 1)
-    return torch.empty_strided(x.shape, strides, dtype=x.dtype, device=x.device)
-
-
 def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, positions=None, eps: float = 1e-6,
                           interleaved: bool = False):
-    """Allocate dq / dk / dq_weight / dk_weight / workspace and run spa_qk_norm_rope_bwd."""
+    """Allocate dq / dk (dense, in the order of q's and k's dimensions) /
+    dq_weight / dk_weight / workspace and run spa_qk_norm_rope_bwd."""
     d = q.shape[-1]
     dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
     ws = q_weight.new_empty(spa_qk_norm_rope_bwd_workspace_bytes(d) // 4)
-    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, _grad_like(q), _grad_like(k), dwq,
-                                dwk, ws, positions, eps, interleaved)
+    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, torch.empty_like(q),
+                                torch.empty_like(k), dwq, dwk, ws, positions, eps, interleaved)
 
 
 class QKNormRopeFunction(torch.autograd.Function):
@@ -829,7 +818,7 @@ class QKNormRopeFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, table, positions, eps, interleaved):
-        q, k = (x if _vector_rows(x) else x.contiguous() for x in (q, k))
+        q, k = (x if _vector_rows(x, x.stride()) else x.contiguous() for x in (q, k))
         ctx.save_for_backward(q, k, q_weight, k_weight, table, positions)
         ctx.eps, ctx.interleaved = eps, interleaved
         return qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions, eps, interleaved)
