@@ -777,20 +777,33 @@ def spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk
     strides of whole 16-byte vectors) and dq_weight, dk_weight (fp32 [d]).
     workspace: CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes."""
     B, Hq, Hk, N, d = _qk_dims(q, k)
-    dt, dev = _dtype_code(q, "q"), q.device
-    ty, q_shape, k_shape = q.dtype, (B, Hq, N, d), (B, Hk, N, d)
-    (pq, sq), (pk, sk) = _need_rows(q, q_shape, ty, dev, "q"), _need_rows(k, k_shape, ty, dev, "k")
-    (pdq, sdq), (pdk, sdk) = _need_rows(dq, q_shape, ty, dev, "dq"), _need_rows(dk, k_shape, ty, dev, "dk")
-    pdqo, pdko = _need_on(dq_out, q_shape, ty, dev, "dq_out"), _need_on(dk_out, k_shape, ty, dev, "dk_out")
-    pqw, pkw, pdqw, pdkw = (_need_on(t, (d,), torch.float32, dev, n) for t, n in (
-        (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight")))
-    if workspace.device != dev or not workspace.is_contiguous() or \
+    _need_rows(dq, (B, Hq, N, d), q.dtype, q.device, "dq")
+    _need_rows(dk, (B, Hk, N, d), q.dtype, q.device, "dk")
+    _need_on(dq_weight, (d,), torch.float32, q.device, "dq_weight")
+    _need_on(dk_weight, (d,), torch.float32, q.device, "dk_weight")
+    if workspace.device != q.device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < spa_qk_norm_rope_bwd_workspace_bytes(d):
         raise ValueError("workspace: contiguous CUDA tensor of spa_qk_norm_rope_bwd_workspace_bytes(d) bytes")
+    return _qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk, dq_weight, dk_weight, workspace,
+                             positions, eps, interleaved, stream)
+
+
+def _qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, dq, dk, dq_weight, dk_weight, workspace,
+                      positions, eps, interleaved, stream=None):
+    """spa_qk_norm_rope_bwd into outputs that are known to fit."""
+    B, Hq, Hk, N, d = _qk_dims(q, k)
+    dt, ty, dev = _dtype_code(q, "q"), q.dtype, q.device
+    q_shape, k_shape = (B, Hq, N, d), (B, Hk, N, d)
+    pq, sq = _need_rows(q, q_shape, ty, dev, "q")
+    pk, sk = _need_rows(k, k_shape, ty, dev, "k")
+    pdqo, pdko = _need_on(dq_out, q_shape, ty, dev, "dq_out"), _need_on(dk_out, k_shape, ty, dev, "dk_out")
+    pqw = _need_on(q_weight, (d,), torch.float32, dev, "q_weight")
+    pkw = _need_on(k_weight, (d,), torch.float32, dev, "k_weight")
     rot, pos, pos_stride = _rope_args(table, positions, B, N, dev)
     _launch(dev, "spa_qk_norm_rope_bwd", _lib.spa_qk_norm_rope_bwd, pdqo, pdko, pq, pk, pqw, pkw, table.data_ptr(), pos,
-            pdq, pdk, pdqw, pdkw, workspace.data_ptr(), B, Hq, Hk, N, d, rot, table.shape[0], pos_stride, sq, sk, sdq,
-            sdk, interleaved, eps, dt, _stream_on(dev, stream))
+            dq.data_ptr(), dk.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), B, Hq, Hk,
+            N, d, rot, table.shape[0], pos_stride, sq, sk, _Strides3(*dq.stride()[:3]), _Strides3(*dk.stride()[:3]),
+            interleaved, eps, dt, _stream_on(dev, stream))
     return dq, dk, dq_weight, dk_weight
 
 
@@ -806,11 +819,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, posit
                           interleaved: bool = False):
     """Allocate dq / dk (dense, in the order of q's and k's dimensions) /
     dq_weight / dk_weight / workspace and run spa_qk_norm_rope_bwd."""
-    d = q.shape[-1]
-    dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
-    ws = q_weight.new_empty(spa_qk_norm_rope_bwd_workspace_bytes(d) // 4)
-    return spa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, torch.empty_like(q),
-                                torch.empty_like(k), dwq, dwk, ws, positions, eps, interleaved)
+    ws = q_weight.new_empty(spa_qk_norm_rope_bwd_workspace_bytes(q.shape[-1]) // 4, dtype=torch.float32)
+    return _qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, table, torch.empty_like(q), torch.empty_like(k),
+                             torch.empty_like(q_weight), torch.empty_like(k_weight), ws, positions, eps, interleaved)
 
 
 class QKNormRopeFunction(torch.autograd.Function):

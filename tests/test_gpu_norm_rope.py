@@ -403,3 +403,23 @@ def test_append_no_tokens(spa):
     w = torch.ones(64, device=DEV)
     out = spa.paged_append(q, q[:, :1], q[:, 1:], kp, vp, table, cu, kv, w, w, spa.rope_table(32, 64))
     assert out.shape == q.shape and (kp == 7.0).all()
+
+
+@pytest.mark.parametrize("order", ["token", "head", "expanded", "batch_last"])
+def test_gradients_keep_the_layout(spa, order):
+    # dq and dk are dense whatever q and k are views of, and in their order of dimensions
+    B, H, N, d = 2, 3, 20, 64
+    x = torch.randn(B, N, 2 * H, d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    q = {"token": lambda: x[:, :, :H].transpose(1, 2), "head": lambda: x[:, :, :H].transpose(1, 2).contiguous(),
+         "expanded": lambda: x[:, :, :1].transpose(1, 2).expand(B, H, N, d),
+         "batch_last": lambda: x[:, :, :H].permute(1, 2, 0, 3).contiguous().permute(2, 1, 0, 3)}[order]()
+    w, table = torch.ones(d, device=DEV), spa.rope_table(N, d)
+    dq = torch.randn(B, H, N, d, generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    got = spa.qk_norm_rope_backward(dq, dq, q, q, w, w, table)
+    want = spa.qk_norm_rope_backward(dq, dq, q.contiguous(), q.contiguous(), w, w, table)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    span = sum((n - 1) * s for n, s in zip(got[0].shape, got[0].stride())) + 1
+    assert span == got[0].numel()
+    if order == "token":
+        assert got[0].transpose(1, 2).is_contiguous()
