@@ -108,15 +108,16 @@ constexpr int kPagedMaxCtas = 296;
 
 // One CTA.  Cuts the line into ctas runs and clears the arrival counts.  Every
 // thread sums a share of the items; after a scan it knows where its share lies
-// in the line and places the cuts that fall into it.  Where the longest run of
-// as many whole items as there are per CTA is no longer than an even run and
-// the cost of dividing items, no item is divided.
+// in the line and places the cuts that fall into it.  First at the nearest
+// ends of items: where the longest run is then no longer than an even run and
+// what dividing items costs, no item is divided.
 template <int TK>
 __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kWarps = kPagedPlanThreads / 32;
   __shared__ long long s_sum[kWarps];
-  __shared__ int s_most[kWarps], s_used[kWarps];
+  __shared__ int s_most[kWarps];
   __shared__ int s_item[kPagedMaxCtas + 1], s_off[kPagedMaxCtas + 1];
+  __shared__ long long s_at[kPagedMaxCtas + 1];  // where the cuts at ends of items lie
   // the kernel that follows may be launched: it waits for this one to end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int items = p.B * p.ng * p.nblk;
@@ -128,64 +129,40 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
     return c ? c + p.piece_cost : 0;
   };
   for (int c = threadIdx.x; c < 2 * p.ctas; c += kPagedPlanThreads) p.arrived[c] = 0;
-  for (int c = threadIdx.x; c <= p.ctas; c += kPagedPlanThreads) {
-    s_item[c] = items;
-    s_off[c] = 0;
-  }
   long long mine = 0;
-  int most = 0, only = 0, used = 0;  // used: items that are not empty
+  int most = 0, only = 0;
   for (int i = i0; i < i1; ++i) {
     only = length(i);
     mine += only;
     most = max(most, only);
-    used += only > 0;
   }
   long long incl = mine;
-  int incl_used = used;
 #pragma unroll
   for (int m = 1; m < 32; m *= 2) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, m);
-    const int u = __shfl_up_sync(0xffffffffu, incl_used, m);
-    if (lane >= m) {
-      incl += v;
-      incl_used += u;
-    }
+    if (lane >= m) incl += v;
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) {
-    s_sum[warp] = incl;
-    s_used[warp] = incl_used;
-  }
+  if (lane == 31) s_sum[warp] = incl;
   if (lane == 0) s_most[warp] = most;
   __syncthreads();
   long long before = incl - mine, total = 0;
-  int before_used = incl_used - used, all_used = 0;
   most = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      before += s_sum[w];
-      before_used += s_used[w];
-    }
+    if (w < warp) before += s_sum[w];
     total += s_sum[w];
-    all_used += s_used[w];
     most = max(most, s_most[w]);
   }
   long long run = total < 2147483647LL - p.ctas ? (long long)(((uint32_t)total + p.ctas - 1) / (uint32_t)p.ctas)
                                                 : (total + p.ctas - 1) / p.ctas;
   run = max(run, (long long)((most + p.max_split - 1) / p.max_split));
   run = max(run, (long long)p.min_run);
-  const int each = (all_used + p.ctas - 1) / p.ctas;  // whole items per CTA
-  if ((long long)each * most <= run + p.split_cost) {
-    for (int i = i0, u = before_used; used > 0 && i < i1; ++i) {
-      if ((per == 1 ? only : length(i)) == 0) continue;
-      if (u % each == 0 && u / each <= p.ctas) s_item[u / each] = i;
-      ++u;
-    }
-  } else if (mine > 0) {
-    // the first cut at or behind the share's beginning
-    int c = before + run < 2147483647LL ? (int)(((uint32_t)before + (uint32_t)run - 1) / (uint32_t)run)
-                                        : (int)((before + run - 1) / run);
+  // the first cut at or behind the share's beginning
+  const int c0 = before + run < 2147483647LL ? (int)(((uint32_t)before + (uint32_t)run - 1) / (uint32_t)run)
+                                             : (int)((before + run - 1) / run);
+  auto place_cuts = [&](bool divide) {
+    int c = c0;
     long long at = run * c, x = before;
     for (int i = i0; i < i1 && at < before + mine; ++i) {
       const int len = per == 1 ? only : length(i);
@@ -193,13 +170,26 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
         // a piece of no or one key tile is not worth its beginning: the cut
         // moves to the item's start or end
         const int off = (int)(at - x) - p.piece_cost;
-        const bool start = off < 2, end = !start && len - p.piece_cost - off < 2;
+        const bool start = divide ? off < 2 : 2 * (at - x) < len;
+        const bool end = !start && (!divide || len - p.piece_cost - off < 2);
         s_item[c] = end ? i + 1 : i;
         s_off[c] = start || end ? 0 : off;
+        s_at[c] = end ? x + len : x;
       }
       x += len;
     }
-  }
+  };
+  for (int c = threadIdx.x; c <= p.ctas; c += kPagedPlanThreads)
+    if (run * c >= total) {
+      s_item[c] = items;
+      s_off[c] = 0;
+      s_at[c] = total;
+    }
+  place_cuts(false);
+  __syncthreads();
+  if (__syncthreads_or((int)threadIdx.x < p.ctas &&
+                       s_at[threadIdx.x + 1] - s_at[threadIdx.x] > run + p.split_cost))
+    place_cuts(true);
   __syncthreads();
   if ((int)threadIdx.x <= p.ctas) {
     // the cuts within the same item, by bisection: (item, off > 0) never falls

@@ -1578,7 +1578,7 @@ int spa_paged_attn(const void* q, const void* k_pages, const void* v_pages, cons
   int group = 1;
   while (same && group < 128 && per_kv % (2 * group) == 0) group *= 2;
   p.piece_cost = 2;
-  p.split_cost = 5;
+  p.split_cost = 6;
   p.min_run = 4;
   p.max_split = kPagedLongSplit;
   if ((st = paged_items(p, bands, group, 256 / group))) return st;
