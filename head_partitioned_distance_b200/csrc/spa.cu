@@ -810,7 +810,7 @@ int make_page_map(CUtensorMap* m, const void* ptr, int64_t pages, int Hk, int pa
 // The kernel for many rows has one CTA per SM.
 constexpr int kPagedShortCtas = 296, kPagedLongCtas = 148;
 // workspace: the plan's cuts, the arrival counts, the partials
-constexpr size_t kPagedPlanBytes = 5120, kPagedHeadBytes = kPagedPlanBytes + 3072;
+constexpr size_t kPagedPlanBytes = 5120, kPagedHeadBytes = kPagedPlanBytes + 4096;
 static_assert(kPagedShortCtas <= spa::kPagedMaxCtas && kPagedLongCtas <= spa::kPagedMaxCtas, "runs");
 static_assert((spa::kPagedMaxCtas + 1) * sizeof(int4) <= kPagedPlanBytes, "cuts");
 static_assert(2 * spa::kPagedMaxCtas * sizeof(int32_t) <= kPagedHeadBytes - kPagedPlanBytes, "arrival counts");
