@@ -90,7 +90,11 @@ __device__ __forceinline__ int head_of(const int32_t* start, int H, int r) {
 // The library's device error word: a kernel that times out on a wait stores
 // kStatusTimeout here, one that meets a device-side index out of its range
 // (a page, a position) kStatusInval; spa_device_status() reads and clears it.
+// The codes rise with their gravity and the word keeps the gravest: after a
+// timeout outputs are incomplete, whatever a later call reports.
 __device__ int g_spa_status;
+
+__device__ __forceinline__ void report_status(int status) { atomicMax(&g_spa_status, status); }
 
 // Bounded wait on one mbarrier phase.  Returns false when the CTA aborted:
 // either this wait ran past kWaitLimitNs (it then raises the CTA's abort flag
@@ -107,7 +111,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
     if (*abort_flag) return false;
     if (ptx::globaltimer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
-      atomicExch(&g_spa_status, kStatusTimeout);
+      report_status(kStatusTimeout);
       return false;
     }
   }
@@ -119,7 +123,7 @@ __device__ __forceinline__ bool bar_drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!ptx::mbar_try_wait(a, parity)) {
     if (ptx::globaltimer_ns() - t0 > kDrainLimitNs) {
-      atomicExch(&g_spa_status, kStatusTimeout);
+      report_status(kStatusTimeout);
       return false;
     }
   }
@@ -138,7 +142,7 @@ __device__ __forceinline__ bool smem_fits(const uint8_t* raw, const uint8_t* ali
   uint32_t dyn;
   asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
   const bool fits = (uint32_t)(aligned - raw) + used <= dyn;
-  if (!fits && threadIdx.x == 0) atomicExch(&g_spa_status, kStatusUnsupported);
+  if (!fits && threadIdx.x == 0) report_status(kStatusUnsupported);
   return fits;
 }
 

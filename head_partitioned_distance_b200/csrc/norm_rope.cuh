@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kNrThreads) spa_paged_append_kernel(const __gr
         slot = ((page * p.Hk) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
     }
     // a position without a table row or a page: nothing is cached for it
-    if (slot < 0 && sub == 0) atomicExch(&g_spa_status, kStatusInval);
+    if (slot < 0 && sub == 0) report_status(kStatusInval);
   }
   const LaneColumns<NEIGHBOURS> lc(sub, p.rot);
   const HeadChunk hc(blockIdx.y, p.heads_per_group, p.Hq, p.Hk, p.Hk);

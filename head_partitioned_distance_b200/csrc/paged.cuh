@@ -357,7 +357,7 @@ struct PagedPages {
         id = p.page_table[(int64_t)it.b * p.width + (j >> p.page_shift)];
         if (id < 0 || id >= p.pages) {
           id = -1;
-          atomicExch(&g_spa_status, kStatusInval);
+          report_status(kStatusInval);
         }
       }
     }
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(160, 2)
     int g = 0;
     bool ok = true;
     while (ok && w.next()) {
-      if (lane == 0 && p.kv_len[w.it.b] > w.it.kv) atomicExch(&g_spa_status, kStatusInval);
+      if (lane == 0 && p.kv_len[w.it.b] > w.it.kv) report_status(kStatusInval);
       const int hk = w.it.hg / p.kv_div;
       for (int t = w.t0; t < w.t1; ++t, ++g) {
         const int s = g % C::NS;

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(384, 1)
       while (ok && w.next()) {
         const PagedItem& it = w.it;
         const int hk = it.hg / p.kv_div;
-        if (lane == 0 && p.kv_len[it.b] > it.kv) atomicExch(&g_spa_status, kStatusInval);
+        if (lane == 0 && p.kv_len[it.b] > it.kv) report_status(kStatusInval);
         // one 128-key tile of K or V into a stage, a box per page and 64 columns
         auto fetch = [&](const CUtensorMap* map, uint32_t at, uint64_t* bar, int t, int id) {
           if (lane == 0) ptx::mbar_arrive_expect_tx(bar, C::KV_BYTES);

@@ -431,8 +431,10 @@ SPA_API int spa_debug_wait_timeout(int64_t limit_ns, void* stream);
 
 /*
  * Synchronises `stream` and returns the library's device error word, then
- * clears it: SPA_OK; SPA_ERR_TIMEOUT when a kernel gave up on a wait (the
- * kernel then wrote incomplete outputs and released its tensor memory); 
+ * clears it (of several reports since the last call the gravest: a timeout,
+ * then unsupported, then inval): SPA_OK; SPA_ERR_TIMEOUT when a kernel gave up
+ * on a wait (the kernel then wrote incomplete outputs and released its tensor
+ * memory);
  * SPA_ERR_INVAL when a kernel met an index in device memory that lies outside
  * its range (a page or position of the paged calls, which say what they do
  * with it); or SPA_ERR_UNSUPPORTED when a kernel found its dynamic shared

@@ -374,3 +374,26 @@ def test_no_rows(spa):
     c.T = 0
     o, lse = c.run(spa)
     assert o.shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_pending_timeout_stays_reported(spa, new):
+    # a later call with a wrong page must not hide that an earlier kernel gave
+    # up on a wait: the status word keeps the gravest report
+    c = Case([(new, 200)], 16, 2, 1, 64, BF, "full", seed=4)
+    c.table[0, 3] = -1
+    assert spa.spa_device_status() == spa.SPA_OK
+    spa.spa_debug_wait_timeout(1_000_000)  # 1 ms
+    c.run(spa)
+    assert spa.spa_device_status() == spa.SPA_ERR_TIMEOUT
+    assert spa.spa_device_status() == spa.SPA_OK
+    c.kv[0] = 16 * c.table.shape[1] + 5
+    spa.spa_debug_wait_timeout(1_000_000)
+    c.run(spa)
+    assert spa.spa_device_status() == spa.SPA_ERR_TIMEOUT
+    rope, w = spa.rope_table(8, 64), torch.ones(64, device=DEV)  # too short for the positions
+    k = torch.zeros(c.T, 1, 64, dtype=BF, device=DEV)
+    spa.spa_debug_wait_timeout(1_000_000)
+    spa.paged_append(c.qd, k, k, c.kp, c.vp, c.table, c.cu, c.kv, w, w, rope)
+    assert spa.spa_device_status() == spa.SPA_ERR_TIMEOUT
+    assert spa.spa_device_status() == spa.SPA_OK
