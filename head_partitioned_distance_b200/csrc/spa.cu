@@ -932,7 +932,8 @@ int paged_items(spa::PagedParams& p, const AttnParams& bands, int group, int tok
     p.lo[g] = bands.lo[g * group];
     p.hi[g] = bands.hi[g * group];
   }
-  return (int64_t)p.B * p.ng * p.nblk > 2147483647LL ? SPA_ERR_UNSUPPORTED : SPA_OK;
+  // the plan's threads round their shares of the list up in 32 bits
+  return (int64_t)p.B * p.ng * p.nblk > 2147483647LL - spa::kPagedPlanThreads ? SPA_ERR_UNSUPPORTED : SPA_OK;
 }
 
 }  // namespace

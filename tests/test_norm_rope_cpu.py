@@ -144,3 +144,13 @@ def test_paged_attention_refuses():
     p[6], p[8] = P, _fake((1 << 20) + 128)
     assert att(p) == spa.SPA_ERR_UNSUPPORTED
     assert spa.spa_paged_attn_workspace_bytes(0, 64) == spa.spa_paged_attn_workspace_bytes(1, 96) == 0
+
+
+@pytest.mark.parametrize("B,Hq,blocks", [(65534, 1, 32769), (64219, 32, 1045), (53965, 101, 394)])
+def test_paged_attention_refuses_lists_at_the_32_bit_border(B, Hq, blocks):
+    # the plan's 512 threads round their shares up: a list this close to 2^31
+    # items would pass it on the way
+    assert 2 ** 31 - 1 - 512 < B * Hq * blocks < 2 ** 31
+    rows = 256 * blocks
+    assert spa._lib.spa_paged_attn(*[P] * 9, B, rows, rows, Hq, Hq, 10, 16, 3, 4096, 64, 0.1, None, None, 0,
+                                   None) == spa.SPA_ERR_UNSUPPORTED
