@@ -96,6 +96,12 @@ __device__ int g_spa_status;
 
 __device__ __forceinline__ void report_status(int status) { atomicMax(&g_spa_status, status); }
 
+// Sequences packed as token rows [cu_q[b], cu_q[b + 1]) of T that name rows
+// which do not exist: those are left out, and one thread of the grid says so.
+__device__ __forceinline__ void report_missing_rows(const int32_t* cu_q, int B, int T) {
+  if (cu_q[0] < 0 || cu_q[B] > T) report_status(kStatusInval);
+}
+
 // Bounded wait on one mbarrier phase.  Returns false when the CTA aborted:
 // either this wait ran past kWaitLimitNs (it then raises the CTA's abort flag
 // and the device error word) or another thread already raised the flag.

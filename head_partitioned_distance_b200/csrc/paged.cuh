@@ -444,6 +444,7 @@ __global__ void __launch_bounds__(160, 2)
     PagedPages pages;
     int g = 0;
     bool ok = true;
+    if (blockIdx.x == 0 && lane == 0) report_missing_rows(p.cu_q, p.B, p.T);
     while (ok && w.next()) {
       if (lane == 0 && p.kv_len[w.it.b] > w.it.kv) report_status(kStatusInval);
       const int hk = w.it.hg / p.kv_div;

@@ -524,6 +524,8 @@ SPA_API int spa_rope_table(float* table, int64_t length, int rot, double base, v
  * included, so that its new token rows stand at positions
  * kv_len[b] - (cu_q[b + 1] - cu_q[b]) .. kv_len[b] - 1.  Token rows from
  * cu_q[B] up to T belong to no sequence; what the outputs hold there stays.
+ * Where cu_q names rows from T on (or below 0) the rows that exist are treated
+ * as usual, and spa_device_status reports SPA_ERR_INVAL.
  * page is a power of two from 16 to 256.
  */
 

@@ -397,3 +397,35 @@ def test_a_pending_timeout_stays_reported(spa, new):
     spa.paged_append(c.qd, k, k, c.kp, c.vp, c.table, c.cu, c.kv, w, w, rope)
     assert spa.spa_device_status() == spa.SPA_ERR_TIMEOUT
     assert spa.spa_device_status() == spa.SPA_OK
+
+
+@pytest.mark.parametrize("new,T", [(1, 1), (9, 15), (9, 9), (40, 61), (40, 40)])
+def test_sequences_past_the_last_row_are_reported(spa, new, T):
+    # cu_q on the device names more token rows than the call has: the rows that
+    # exist are right, and the status says that some are missing
+    c = Case([(new, 200), (new, 100)], 16, 2, 1, 64, BF, "full", seed=6, pad=0)
+    c.qd, c.T = c.qd[:T].contiguous(), T
+    assert spa.spa_device_status() == spa.SPA_OK
+    o, lse = c.run(spa)
+    assert spa.spa_device_status() == spa.SPA_ERR_INVAL
+    c.check(o, lse, rows=set(range(T)))
+    w, rope = torch.ones(64, device=DEV), spa.rope_table(200, 64)
+    k = torch.randn(T, 1, 64, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    table = torch.arange(26, dtype=torch.int32, device=DEV).view(2, 13)
+    kp, vp = torch.full((26, 1, 16, 64), 7.0, dtype=BF, device=DEV), torch.full((26, 1, 16, 64), 7.0, dtype=BF, device=DEV)
+    q = spa.paged_append(c.qd, k, k, kp, vp, table, c.cu, c.kv, w, w, rope)
+    assert spa.spa_device_status() == spa.SPA_ERR_INVAL
+    assert (q != 0).flatten(1).any(1).all()
+    flat = vp.view(2, -1, 64)  # [sequence][position]
+    first = min(new, T)
+    assert torch.equal(flat[0, 200 - new:200 - new + first], k[:first, 0])
+    assert torch.equal(flat[1, 100 - new:100 - new + T - first], k[first:, 0])
+    assert int((flat != 7.0).any(-1).sum()) == T
+    # rows of no sequence in front: left as they are, and no error
+    c = Case([(new, 200), (new, 100)], 16, 2, 1, 64, BF, "full", seed=7, pad=0)
+    c.cu, c.T = c.cu + 2, c.T + 2
+    c.qd = torch.cat((torch.full_like(c.qd[:2], float("nan")), c.qd))
+    o, lse = c.run(spa)
+    assert spa.spa_device_status() == spa.SPA_OK
+    assert (o[:2] == 3.0).all() and (lse[:2] == 5.0).all()
+    c.check(o[2:], lse[2:], rows=set(range(2 * new)))
