@@ -936,9 +936,14 @@ def spa_paged_attn(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, o,
 def paged_attention(q, k_pages, v_pages, page_table, cu_q, kv_len, max_q: int, scale=None, lo=None, hi=None, N=None,
                     out=None, lse=None):
     """Attention of the new tokens (one or many per sequence) over the paged
-    cache; allocates o / lse (unless given as out, lse; rows behind the last
-    sequence are not written) and the workspace and runs spa_paged_attn.  N,
-    the length the bands belong to, defaults to what the page table can hold."""
+    cache; allocates o / lse (unless given as out, lse) and the workspace and
+    runs spa_paged_attn.  max_q: no sequence may have more new tokens; rows past
+    that many of a sequence, and rows behind the last sequence, are not written.
+    N: the length that the model's bands belong to; it may be left out where lo
+    and hi give the bands (it then only bounds them: what the page table can
+    hold)."""
+    if N is None and (lo is None or hi is None):
+        raise ValueError("N: without both lo and hi the bands follow from the length that the model was trained with")
     d = q.shape[-1]
     scale = d ** -0.5 if scale is None else scale
     N = page_table.shape[-1] * k_pages.shape[2] if N is None else N

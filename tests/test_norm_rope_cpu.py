@@ -154,3 +154,17 @@ def test_paged_attention_refuses_lists_at_the_32_bit_border(B, Hq, blocks):
     rows = 256 * blocks
     assert spa._lib.spa_paged_attn(*[P] * 9, B, rows, rows, Hq, Hq, 10, 16, 3, 4096, 64, 0.1, None, None, 0,
                                    None) == spa.SPA_ERR_UNSUPPORTED
+
+
+def test_paged_attention_asks_for_the_length_of_the_bands():
+    # the balanced bands belong to the model's length; the capacity of the page
+    # table (16 * 3 here) is not that, and changes when the table grows
+    q, kp = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 4, 16, 64, dtype=torch.bfloat16)
+    table, cu, kv = (torch.zeros(s, dtype=torch.int32) for s in ((1, 3), (2,), (1,)))
+    for bands in ({}, {"lo": [0] * 4}, {"hi": [9] * 4}):
+        with pytest.raises(ValueError, match="length that the model was trained with"):
+            spa.paged_attention(q, kp, kp, table, cu, kv, 2, **bands)
+    # given the length, or the bands, the call goes on to its other checks
+    for more in ({"N": 48}, {"lo": [0] * 4, "hi": [9] * 4}):
+        with pytest.raises(ValueError, match="CUDA"):
+            spa.paged_attention(q, kp, kp, table, cu, kv, 2, **more)
