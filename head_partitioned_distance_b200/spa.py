@@ -824,12 +824,21 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, table, posit
                              torch.empty_like(q_weight), torch.empty_like(k_weight), ws, positions, eps, interleaved)
 
 
+def _dense(t):
+    """t contiguous and on a 16-byte border: itself, or a copy (a part of a longer
+    tensor may be contiguous and start anywhere)."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class QKNormRopeFunction(torch.autograd.Function):
     """Norm and rotation of queries and keys as an autograd function."""
 
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, table, positions, eps, interleaved):
-        q, k = (x if _vector_rows(x, x.stride()) else x.contiguous() for x in (q, k))
+        q, k = (x if _vector_rows(x, x.stride()) else _dense(x) for x in (q, k))
+        q_weight, k_weight, table = _dense(q_weight), _dense(k_weight), _dense(table)
         ctx.save_for_backward(q, k, q_weight, k_weight, table, positions)
         ctx.eps, ctx.interleaved = eps, interleaved
         return qk_norm_rope_forward(q, k, q_weight, k_weight, table, positions, eps, interleaved)
@@ -838,7 +847,7 @@ class QKNormRopeFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
-        grads = qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight, table,
+        grads = qk_norm_rope_backward(_dense(dq_out), _dense(dk_out), q, k, q_weight, k_weight, table,
                                       positions, ctx.eps, ctx.interleaved)
         return (*grads, None, None, None, None)
 

@@ -423,3 +423,35 @@ def test_gradients_keep_the_layout(spa, order):
     assert span == got[0].numel()
     if order == "token":
         assert got[0].transpose(1, 2).is_contiguous()
+
+
+def test_autograd_takes_values_off_a_vector_border(spa):
+    # gradients that arrive as parts of a longer one, and weights that are parts
+    # of a flat parameter, start anywhere; so may rows of q and k that are dense
+    B, H, N, d = 1, 3, 21, 64
+    q, k, wq, wk = make(B, H, 1, N, d, torch.bfloat16, 31, "head")
+    table = spa.rope_table(N, d)
+    g = torch.Generator().manual_seed(32)
+    dq, dk = (torch.randn(t.shape, generator=g).to(torch.bfloat16).to(DEV) for t in (q, k))
+
+    def off(t, by):  # the same values, contiguous, `by` elements behind a border
+        flat = t.new_empty(t.numel() + by)
+        flat[by:] = t.flatten()
+        return flat[by:].view(t.shape)
+
+    want = spa.qk_norm_rope_forward(q, k, wq, wk, table)
+    want_g = spa.qk_norm_rope_backward(dq, dk, q, k, wq, wk, table)
+    for by in (1, 3):
+        leaves = [off(t, by).requires_grad_() for t in (q, k, wq, wk)]
+        assert all(t.data_ptr() % 16 for t in leaves)
+        out = spa.qk_norm_rope(*leaves, off(table, by))
+        got = torch.autograd.grad(out, leaves, (off(dq, by), off(dk, by)))
+        for a, b in zip(out + got, want + want_g):
+            assert torch.equal(a, b)
+    # as it happens: both outputs joined behind something of odd length
+    leaves = [t.detach().clone().requires_grad_() for t in (q, k, wq, wk)]
+    qn, kn = spa.qk_norm_rope(*leaves, table)
+    long = torch.cat((qn.new_zeros(3), qn.flatten(), kn.flatten()))
+    got = torch.autograd.grad(long, leaves, torch.cat((dq.new_ones(3), dq.flatten(), dk.flatten())))
+    for a, b in zip(got, want_g):
+        assert torch.equal(a, b)
