@@ -744,6 +744,8 @@ def spa_rope_table(table, base: float, stream=None):
 
 def rope_table(length: int, rot: int, base: float = 10000.0, device=None):
     """The rotation's table for positions [0, length) and rot rotated columns."""
+    if rot % 2:
+        raise ValueError(f"rot: columns are rotated in pairs, got {rot}")
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     return spa_rope_table(torch.empty((length, rot // 2, 2), dtype=torch.float32, device=device), base)
 

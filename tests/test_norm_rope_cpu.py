@@ -168,3 +168,10 @@ def test_paged_attention_asks_for_the_length_of_the_bands():
     for more in ({"N": 48}, {"lo": [0] * 4, "hi": [9] * 4}):
         with pytest.raises(ValueError, match="CUDA"):
             spa.paged_attention(q, kp, kp, table, cu, kv, 2, **more)
+
+
+@pytest.mark.parametrize("rot", [17, 33, 129])
+def test_rope_table_refuses_odd_columns(rot):
+    # not the table of one column less
+    with pytest.raises(ValueError, match="pairs"):
+        spa.rope_table(10, rot, device="cpu")
