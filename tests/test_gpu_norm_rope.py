@@ -455,3 +455,58 @@ def test_autograd_takes_values_off_a_vector_border(spa):
     got = torch.autograd.grad(long, leaves, torch.cat((dq.new_ones(3), dq.flatten(), dk.flatten())))
     for a, b in zip(got, want_g):
         assert torch.equal(a, b)
+
+
+def test_the_kernels_gradient_against_differences(spa):
+    # the slope that the backward's outputs give along random directions of x
+    # and both weights, against central differences of the formula in fp64
+    # (step 1e-5: error 1e-6 of the slope's scale); each output may be off by
+    # its tolerance above, times the direction's magnitude there
+    B, Hq, Hk, N, d, rot, eps = 1, 3, 2, 11, 64, 48, 1e-5
+    for il, dtype in ((False, torch.bfloat16), (True, torch.float16)):
+        q, k, wq, wk = make(B, Hq, Hk, N, d, dtype, 51)
+        g = torch.Generator().manual_seed(52)
+        dqo = torch.randn(B, Hq, N, d, generator=g).to(dtype).to(DEV)
+        dko = torch.randn(B, Hk, N, d, generator=g).to(dtype).to(DEV)
+        table = spa.rope_table(N, rot)
+        dq, dk, dwq, dwk = spa.qk_norm_rope_backward(dqo, dko, q, k, wq, wk, table, None, eps, il)
+        cs, ok = table.double().cpu(), torch.ones(1, 1, N, 1)
+        for dx, dw, dy, x, w in ((dq, dwq, dqo, q, wq), (dk, dwk, dko, k, wk)):
+            dx, dw, dy, x, w = (t.detach().double().cpu() for t in (dx, dw, dy, x, w))
+            f = lambda x_, w_: (ref_fwd(x_, w_, cs, eps, il)[0] * dy).sum()  # noqa: E731
+            _, mag, _, dw_mag = ref_bwd(dy, x, w, cs, eps, il, ok)
+            off = HALF[dtype] * dx.abs() * 1.01 + 4e-6 * mag + 2.0 ** -25
+            for _ in range(3):
+                u, v = torch.randn(x.shape, generator=g).double(), torch.randn(d, generator=g).double()
+                h = 1e-5
+                diff = (f(x + h * u, w + h * v) - f(x - h * u, w - h * v)) / (2 * h)
+                tol = (off * u.abs()).sum() + (1e-5 * dw_mag * v.abs()).sum() + 1e-6 * (1 + diff.abs())
+                assert abs((dx * u).sum() + (dw * v).sum() - diff) <= tol
+                # a direction of one element each: where no sum hides a wrong sign
+                for i in torch.randint(0, x.numel(), (8,), generator=g).tolist():
+                    e = torch.zeros(x.numel()).double()
+                    e[i] = 1
+                    e = e.view(x.shape)
+                    diff = (f(x + h * e, w) - f(x - h * e, w)) / (2 * h)
+                    assert abs((dx * e).sum() - diff) <= (off * e).sum() + 1e-6 * (1 + diff.abs())
+
+
+def test_append_beside_refused_tokens(spa):
+    # tokens without a place leave the others' rows, keys and values right
+    table, cu, kv, kp, vp = paged([(2, 20), (3, 5), (1, 30), (2, 3)], 16, 2, 64, torch.bfloat16, 1, fill=7.0)
+    table[0, 1] = kp.shape[0]  # positions 18 and 19 of the first sequence
+    q, k, wq, wk = make(1, 4, 2, 8, 64, torch.bfloat16, 3)
+    q, k = q[0].transpose(0, 1), k[0].transpose(0, 1)
+    v = torch.randn(8, 2, 64, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
+    rope = spa.rope_table(30, 64)
+    out = spa.paged_append(q, k, v, kp, vp, table, cu, kv, wq, wk, rope, 1e-5)
+    assert spa.spa_device_status() == spa.SPA_ERR_INVAL
+    assert (out[:2] == 0).all()
+    pos = [2, 3, 4, 29, 1, 2]
+    cs = rope.double().cpu()[pos][:, None]
+    check_fwd(out[2:], q[2:].double().cpu(), wq.double().cpu(), cs, 1e-5, False)
+    seq = [1, 1, 1, 2, 3, 3]
+    page, at = [int(table[s, p // 16]) for s, p in zip(seq, pos)], [p % 16 for p in pos]
+    check_fwd(kp[page, :, at], k[2:].double().cpu(), wk.double().cpu(), cs, 1e-5, False)
+    assert torch.equal(vp[page, :, at], v[2:])
+    assert int((vp != 7.0).flatten(2).any(-1).sum()) <= 6 * 2 and int((vp[:, 0] != 7.0).any(-1).sum()) == 6

@@ -429,3 +429,83 @@ def test_sequences_past_the_last_row_are_reported(spa, new, T):
     assert spa.spa_device_status() == spa.SPA_OK
     assert (o[:2] == 3.0).all() and (lse[:2] == 5.0).all()
     c.check(o[2:], lse[2:], rows=set(range(2 * new)))
+
+
+@pytest.mark.parametrize("seqs,page,Hq,Hk,d,dtype,kind", [
+    ([(1, 9), (1, 33), (1, 80)], 16, 8, 2, 64, BF, "full"),
+    ([(1, 700), (1, 40)], 32, 8, 8, 128, BF, "window24"),
+    ([(4, 30), (3, 300)], 64, 8, 2, 128, BF, "window50"),
+    ([(1, 9), (1, 33), (1, 80)], 16, 8, 2, 128, FP, "full"),
+    ([(1, 9000), (1, 20)], 64, 4, 1, 64, BF, "full"),
+])
+def test_few_rows_keep_p_in_two_terms(spa, seqs, page, Hq, Hk, d, dtype, kind):
+    """The kernel for few rows multiplies V by P in two 16-bit terms.  The
+    second is the first's error, at most h p, and is off by h of itself, so P
+    is off by h^2 p (fp16: or half the smallest subnormal, 2^-25), not by h p:
+      |o - ref| <= h |o| + (h^2 + 2e-5 + e_s) A + 2^-25 (n max|v| + 1) for fp16.
+    Every second value is close to the opposite of the one before, so that |o|
+    is far below A; P rounded once, formed here in fp64, has to miss the bound."""
+    c = Case(seqs, page, Hq, Hk, d, dtype, kind, seed=41)
+    h16, scale, G = HALF[dtype], d ** -0.5, Hq // Hk
+    for s, (n, length) in enumerate(seqs):
+        even = length // 2 * 2
+        c.v[s][:, 1:even:2] = -c.v[s][:, 0:even:2] * (1 + 2.0 ** -5)
+        for i in range(-(-length // page)):  # what is attended to; NaN stays where it is
+            if c.table[s, i] < 0:
+                continue
+            m = min(page, length - i * page)
+            place = c.vp[int(c.table[s, i]), :, :m]
+            place.copy_(torch.where(place.isnan(), place, c.v[s][:, i * page:i * page + m].to(DEV)))
+    o, lse = (t.double().cpu() for t in c.run(spa))
+    t0, missed = 0, False
+    for s, (n, length) in enumerate(seqs):
+        gap = torch.arange(length - n, length)[:, None] - torch.arange(length)
+        for h in range(Hq):
+            k, v = c.k[s][h // G].double(), c.v[s][h // G].double()
+            q = c.q[t0:t0 + n, h].double()
+            ok = (gap >= c.lo[h]) & (gap < c.hi[h])
+            x = torch.where(ok, q @ k.T * scale, -math.inf)
+            e_s = torch.where(ok, q.abs() @ k.abs().T, 0.0).amax(-1) * scale * 2.0 ** -17
+            p = torch.exp(x - x.amax(-1, keepdim=True))
+            total = p.sum(-1, keepdim=True)
+            want, mag = p @ v / total, p @ v.abs() / total
+            tol = h16 * want.abs() + (h16 * h16 + 2e-5 + e_s[:, None]) * mag
+            if dtype == FP:
+                tol = tol + 2.0 ** -25 * (ok.sum(-1)[:, None] * v.abs().max() + 1)
+            err = (o[t0:t0 + n, h] - want).abs()
+            assert (err <= tol).all(), (s, h, float((err / tol).max()))
+            assert ((lse[t0:t0 + n, h] - torch.logsumexp(x, -1)).abs() <= e_s + 2e-5).all()
+            missed |= bool(((p.to(dtype).double() @ v / total - want).abs() > tol).any())
+        t0 += n
+    assert missed
+
+
+def test_two_streams_at_once_many_rows(spa):
+    # both kernels and both element types in flight together
+    cases = [Case([(300, 3000), (40, 900)], 16, 8, 2, 64, BF, "full", seed=1),
+             Case([(513, 2000)], 64, 4, 4, 128, FP, "balanced", seed=2),
+             Case([(1, 3000), (1, 2000)], 16, 8, 2, 64, BF, "full", seed=3)]
+    want = [tuple(t.clone() for t in c.run(spa)) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for c, s, g in zip(cases, streams, got):
+            with torch.cuda.stream(s):
+                g.append(c.run(spa))
+    torch.cuda.synchronize()
+    for w, outs in zip(want, got):
+        for o, lse in outs:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    assert spa.spa_device_status() == spa.SPA_OK
+
+
+def test_random_bands_on_heads_that_share_keys(spa):
+    # every query head its own band, four heads to a key/value head
+    for seed, new in ((1, 1), (2, 9), (3, 70)):
+        c = Case([(new, 500), (new, 333), (0, 40), (new, new)], 32, 8, 2, 64, BF, "full", seed=seed, N=512)
+        g = torch.Generator().manual_seed(seed)
+        c.lo = torch.randint(0, 300, (8,), generator=g).tolist()
+        c.hi = [a + int(torch.randint(1, 212, (1,), generator=g)) for a in c.lo]
+        c.check(*c.run(spa))
+    assert spa.spa_device_status() == spa.SPA_OK
