@@ -1,5 +1,5 @@
 // elem.cuh -- the two 16-bit element types of the query/key norm and of the
-// paged cache: packing, unpacking, and rows of 16-byte vectors.
+// paged cache: unpacking, packing, and the store of an fp32 row as 16 bits.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -29,21 +29,6 @@ struct Fp16 {
     return r;
   }
 };
-
-template <class E>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = E::unpack(ptx::word_of(v, e));
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
-  }
-}
-
-template <class E>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(E::pack(x[0], x[1]), E::pack(x[2], x[3]), E::pack(x[4], x[5]), E::pack(x[6], x[7]));
-}
 
 // 32 fp32 values times `mul` -> 32 16-bit values at `dst` (64 bytes, 32-byte
 // aligned).
