@@ -63,7 +63,8 @@ struct PagedItem {
   int jlo, jhi;  // keys that some row attends to (jhi < jlo: none)
   int kv;        // keys the sequence has (and the page table can name)
   int t0;        // first key tile
-  int cost;      // key tiles; an item without keys counts one
+  int cost;      // key tiles; an item without keys counts one, one without rows none
+  int next;      // without rows: how far on the next item is that may have some
 };
 
 // Positions and lengths are 32-bit; sums of them with band limits need more.
@@ -88,6 +89,13 @@ __device__ __forceinline__ PagedItem paged_item(const PagedParams& p, int b, int
   const bool any = it.tokens > 0 && it.jhi >= it.jlo;
   it.t0 = any ? it.jlo / TK : 0;
   it.cost = it.tokens == 0 ? 0 : any ? it.jhi / TK - it.t0 + 1 : 1;
+  // A head group's row blocks behind an empty one are empty too, and a sequence
+  // without rows has none at all.  (Taken one by one, at 0.17 us each, they
+  // could cost more than the attention: a prompt of 8192 tokens gives every
+  // sequence of its batch 128 blocks per head group, and with 15 single tokens
+  // took 3.1 ms instead of 0.5; and over tens of thousands of sequences one
+  // role's steps could have outlasted another's wait.)
+  it.next = (n > 0 ? p.nblk : (p.ng - hg) * p.nblk) - blk;
   return it;
 }
 
@@ -115,7 +123,7 @@ template <int TK>
 __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const __grid_constant__ PagedParams p) {
   constexpr int kWarps = kPagedPlanThreads / 32;
   __shared__ long long s_sum[kWarps];
-  __shared__ int s_most[kWarps];
+  __shared__ int s_most[kWarps], s_end[kWarps];
   __shared__ int s_item[kPagedMaxCtas + 1], s_off[kPagedMaxCtas + 1];
   __shared__ long long s_at[kPagedMaxCtas + 1];  // where the cuts at ends of items lie
   // the kernel that follows may be launched: it waits for this one to end
@@ -124,17 +132,20 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
   const int per = (items + kPagedPlanThreads - 1) / kPagedPlanThreads;
   const int i0 = min((int)threadIdx.x * per, items), i1 = min(i0 + per, items);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int step;  // from the item last asked for to the next that may have rows
   auto length = [&](int i) {
-    const int c = paged_item_at<TK>(p, i).cost;
-    return c ? c + p.piece_cost : 0;
+    const PagedItem it = paged_item_at<TK>(p, i);
+    step = it.cost ? 1 : it.next;
+    return it.cost ? it.cost + p.piece_cost : 0;
   };
   for (int c = threadIdx.x; c < 2 * p.ctas; c += kPagedPlanThreads) p.arrived[c] = 0;
   long long mine = 0;
-  int most = 0, only = 0;
-  for (int i = i0; i < i1; ++i) {
+  int most = 0, only = 0, end = 0;  // end: behind the last item with rows
+  for (int i = i0; i < i1; i += step) {
     only = length(i);
     mine += only;
     most = max(most, only);
+    end = only ? i + 1 : end;
   }
   long long incl = mine;
 #pragma unroll
@@ -143,8 +154,9 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
     if (lane >= m) incl += v;
   }
   most = __reduce_max_sync(0xffffffffu, most);
+  end = __reduce_max_sync(0xffffffffu, end);
   if (lane == 31) s_sum[warp] = incl;
-  if (lane == 0) s_most[warp] = most;
+  if (lane == 0) s_most[warp] = most, s_end[warp] = end;
   __syncthreads();
   long long before = incl - mine, total = 0;
   most = 0;
@@ -153,6 +165,7 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
     most = max(most, s_most[w]);
+    end = max(end, s_end[w]);
   }
   long long run = total < 2147483647LL - p.ctas ? (long long)(((uint32_t)total + p.ctas - 1) / (uint32_t)p.ctas)
                                                 : (total + p.ctas - 1) / p.ctas;
@@ -164,7 +177,7 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
   auto place_cuts = [&](bool divide) {
     int c = c0;
     long long at = run * c, x = before;
-    for (int i = i0; i < i1 && at < before + mine; ++i) {
+    for (int i = i0; i < i1 && at < before + mine; i += step) {
       const int len = per == 1 ? only : length(i);
       for (; at < x + len && c <= p.ctas; at += run, ++c) {
         // a piece of no or one key tile is not worth its beginning: the cut
@@ -181,7 +194,7 @@ __global__ void __launch_bounds__(kPagedPlanThreads) spa_paged_plan_kernel(const
   };
   for (int c = threadIdx.x; c <= p.ctas; c += kPagedPlanThreads)
     if (run * c >= total) {
-      s_item[c] = items;
+      s_item[c] = end;  // what has no rows behind that is nobody's
       s_off[c] = 0;
       s_at[c] = total;
     }
@@ -246,6 +259,7 @@ struct PagedWalk {
       ++item;
       if (item > run.to.item || (item == run.to.item && run.to.off == 0)) return false;
       it = paged_item_at<TK>(p, item);
+      if (it.cost == 0) item += it.next - 1;
     } while (it.cost == 0);
     const int off = item == run.from.item ? run.from.off : 0;
     const int end = item == run.to.item ? run.to.off : it.cost;

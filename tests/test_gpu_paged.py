@@ -509,3 +509,53 @@ def test_random_bands_on_heads_that_share_keys(spa):
         c.hi = [a + int(torch.randint(1, 212, (1,), generator=g)) for a in c.lo]
         c.check(*c.run(spa))
     assert spa.spa_device_status() == spa.SPA_OK
+
+
+def median_ms(spa, case):
+    """Device time of one call, from a graph of eight (no host time in it)."""
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(8):
+            case.run(spa)
+    times = []
+    for _ in range(9):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        graph.replay()
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b) / 8)
+    return sorted(times)[4]
+
+
+def test_long_prompt_among_single_tokens(spa):
+    # max_q gives every sequence the prompt's row blocks, almost all of them
+    # empty: 16 sequences x 8 head groups x 128 blocks, 8 x 15 of which exist
+    # behind the prompt's
+    seqs = [(1, 200)] * 5 + [(8192, 8192)] + [(0, 70), (1, 256)] + [(1, 100)] * 8
+    c = Case(seqs, 64, 32, 8, 64, BF, "window100", seed=12)
+    o, lse = c.run(spa)
+    t0 = 5 + 8192
+    c.check(o, lse, rows=set(range(8)) | {4096, t0 - 1} | set(range(t0, c.T - 2)))
+    assert (o[-2:] == 3.0).all() and (lse[-2:] == 5.0).all()
+    assert spa.spa_device_status() == spa.SPA_OK
+    # 14 single tokens next to 8192 are a fifth of its items and far less of
+    # its work; steps over the empty blocks, one by one, took it several times
+    alone = Case([(8192, 8192)], 64, 32, 8, 64, BF, "window100", seed=12)
+    alone.run(spa)
+    assert median_ms(spa, c) < 3 * median_ms(spa, alone)
+
+
+@pytest.mark.parametrize("order", ["behind", "before", "between"])
+def test_batch_padded_with_idle_sequences(spa, order):
+    # a captured batch of 512 places, 16 of them taken
+    live, idle = [(1, 900 + i) for i in range(16)], [(0, 0)] * 496
+    seqs = {"behind": live + idle, "before": idle + live, "between": live[:15] + idle + live[15:]}[order]
+    c = Case(seqs, 64, 32, 32, 64, BF, "full", seed=13, pad=496)
+    c.check(*c.run(spa))
+    assert spa.spa_device_status() == spa.SPA_OK
+    # the idle places were 15872 items: stepping over each took 20 times as long
+    # as the attention
+    alone = Case(live, 64, 32, 32, 64, BF, "full", seed=13)
+    alone.run(spa)
+    assert median_ms(spa, c) < 6 * median_ms(spa, alone)
