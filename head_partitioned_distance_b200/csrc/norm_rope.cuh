@@ -27,9 +27,9 @@ namespace spa {
 
 constexpr int kNrThreads = 128;
 constexpr int kNrUnroll = 4;        // head rows in flight per lane group
-// Backward: blocks, each one partial of a weight's gradient; 6 per SM, the most
-// that 80 registers allow (B1 H32/8 N30001 d128: 174 us, 5.4 TB/s; 5 per SM 190,
-// 7 with spills 203).
+// Backward: blocks, each one partial of a weight's gradient; 6 per SM, with 80
+// registers and 32 to 40 bytes spilled (B1 H32/8 N30001 d128: 174 us, 5.4 TB/s;
+// 5 per SM, with up to 96 registers and no spills, 190; 7 per SM 203).
 constexpr int kNrMaxBlocks = 888;
 
 struct RowStrides {

@@ -298,9 +298,9 @@ __device__ __forceinline__ int64_t paged_row(const PagedParams& p, const PagedIt
 // the bytes take, and single rows need no tcgen05 tile of 128).  P stays in
 // registers, which its accumulator layout lets serve as the A operand.  The
 // four warps' results meet at the end of a piece.  Measured: 16 sequences of up
-// to 32768 positions, 32 heads on 8 key/value heads, 1.66 GB in 251 us, 6.6
-// TB/s; 8 sequences with 32 bands of 1024, 105 MB in 23 us, most of which is
-// the latency of the first pages and of the end.
+// to 32768 positions, 32 heads on 8 key/value heads, 1.66 GB in 252-260 us, 6.4
+// to 6.6 TB/s; 8 sequences with 32 bands of 1024, 105 MB in 23 us, most of which
+// is the latency of the first pages and of the end.
 template <int D>
 struct PagedShortCfg {
   static constexpr int TK = 64, ROWS = 16, WARPS = 4, NTHREADS = 160, CTAS_PER_SM = 2;

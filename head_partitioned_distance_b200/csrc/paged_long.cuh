@@ -23,7 +23,8 @@
 // special-function lanes), 1350 for the two products (2 x 512 of the tensor
 // core, and the signals between them), against which the other tile's step is
 // set.  4096 tokens of 32 heads over 16384 positions of one key/value head:
-// 1240 TFLOP/s, 75 % of the measured bf16 rate.  Tried and slower there: 64-key
+// 1215 TFLOP/s, 74 % of the measured bf16 rate (1010-1100 over long calls, when
+// the power cap lowers the clocks).  Tried and slower there: 64-key
 // tiles with S ahead of the softmax (the issuing thread's own instructions
 // then take longer than the products: 970), a polynomial for part of the
 // exponentials (more instructions than it saves lanes: 1130 at a quarter), the
@@ -139,6 +140,11 @@ __device__ __forceinline__ void paged_mask32(uint32_t (&s)[32], int lo, int hi) 
 }
 
 // p = 2^(s c2 + mneg) of 32 scores as 16-bit pairs; adds them up in fp32.
+// P is rounded once, as in the training forward.  That adds to o about the error
+// of its own rounding: against fp64, o is off by 2.3e-3 of its norm in bf16 where
+// rounding o alone gives 1.65e-3, and by 2.0e-4 against 1.5e-4 in fp16.  The
+// second term that the kernel for few rows carries would cost half the products
+// again here, where the products bound the step.
 template <class E>
 __device__ __forceinline__ void paged_exp32(const uint32_t (&s)[32], float2 c2v, float2 mnv, float2& sa, float2& sb,
                                             uint32_t (&pk)[16]) {

@@ -860,7 +860,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, table, positions=None, eps: float = 1
     before spattention.  Differentiable in q, k and the weights.  q and k may
     be views of a token-major projection; the outputs are contiguous.  Weights
     of another type are used in fp32.  table: rope_table(...); positions:
-    int32 [N] or [B, N], or None for 0 .. N - 1."""
+    int32 [N] or [B, N], or None for 0 .. N - 1.  As with any autograd function,
+    a backward() captured into a CUDA graph needs leaves that no eager graph
+    still holds."""
     return QKNormRopeFunction.apply(q, k, q_weight.float(), k_weight.float(), table, positions, eps, interleaved)
 
 
@@ -907,7 +909,7 @@ def paged_append(q, k, v, k_pages, v_pages, page_table, cu_q, kv_len, q_weight, 
                  interleaved: bool = False, out=None):
     """Norm and rotate the new tokens' queries and keys, store keys and values in
     the paged cache, return the queries (allocated unless given as out; rows
-    behind the last sequence are not written)."""
+    behind the last sequence are not written).  The weights are fp32."""
     out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
     return spa_paged_append(q, k, v, q_weight, k_weight, table, cu_q, kv_len, page_table, out, k_pages, v_pages, eps,
                             interleaved)

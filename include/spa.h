@@ -469,8 +469,9 @@ typedef enum spa_dtype { SPA_BF16 = 0, SPA_FP16 = 1 } spa_dtype_t;
  *   q_out, k_out: DEVICE, [B][Hq][N][d], [B][Hk][N][d] contiguous, the layout
  *              of spa_attn_fwd; must not overlap the inputs
  * One launch, asynchronous on `stream`.  Sums are fp32, outputs are rounded
- * once.  SPA_ERR_INVAL for null pointers, sizes < 1, eps not finite or < 0,
- * an unknown dtype, N > table_len without positions; SPA_ERR_UNSUPPORTED for d not in {64, 128}, rot not a
+ * once; a row's sum of squares has to lie within fp32.  SPA_ERR_INVAL for null
+ * pointers, sizes < 1, eps not finite or < 0, an unknown dtype, N > table_len
+ * without positions; SPA_ERR_UNSUPPORTED for d not in {64, 128}, rot not a
  * multiple of 16 in [16, d], Hq + Hk > 1024, B * N > 2^31 - 1, tensors not
  * 16-byte aligned (positions: 4) and strides that are not multiples of 8.
  */
@@ -486,7 +487,8 @@ SPA_API int spa_qk_norm_rope_fwd(const void* q, const void* k, const float* wq, 
  *   dq_out, dk_out: gradients of q_out, k_out, contiguous as those
  *   dq, dk:         outputs, written through dq_strides, dk_strides (rules of
  *                   the inputs' strides, and none 0 where its extent is
- *                   above one: no two elements may share memory)
+ *                   above one: no two elements may share memory); no output
+ *                   may overlap an input
  *   dwq, dwk:       outputs, fp32 [d]
  *   workspace:      DEVICE buffer of spa_qk_norm_rope_bwd_workspace_bytes(d)
  *                   bytes, 16-byte aligned, caller-owned, overwritten
@@ -539,9 +541,10 @@ SPA_API int spa_rope_table(float* table, int64_t length, int rot, double base, v
  * A token whose position lies outside the table or the page table's width, or
  * whose page number lies outside [0, pages), gets a zero q_out row and no
  * place in the cache, and spa_device_status reports SPA_ERR_INVAL.  Two tokens
- * must not share a place, and no output may overlap an input.  One launch; T = 0 launches nothing.  Errors as
- * spa_qk_norm_rope_fwd, and SPA_ERR_UNSUPPORTED for a page size outside the
- * rule above, Hq + 2 Hk > 1024 or B > 65535.
+ * must not share a place, and no output may overlap an input.  One launch;
+ * T = 0 launches nothing.  Errors as spa_qk_norm_rope_fwd, and
+ * SPA_ERR_UNSUPPORTED for a page size outside the rule above, Hq + 2 Hk > 1024
+ * or B > 65535.
  */
 SPA_API int spa_paged_append(const void* q, const void* k, const void* v, const float* wq, const float* wk,
                              const float* table, const int32_t* cu_q, const int32_t* kv_len,
@@ -561,12 +564,16 @@ SPA_API int spa_paged_append(const void* q, const void* k, const void* v, const 
  *   q:         DEVICE [T][Hq][d]
  *   o:         DEVICE [T][Hq][d];  lse: DEVICE fp32 [T][Hq], natural log
  *   max_q:     no sequence has more new tokens; rows past that many of one
- *              sequence are not written
+ *              sequence are not written, and the status does not say so.  It
+ *              also chooses the kernel: up to 16 rows of max_q tokens x the
+ *              query heads that share keys, P meets V in two 16-bit terms (o is
+ *              as exact as its own rounding); above, in one
  *   N, lo, hi: length of the bands: HOST arrays of Hq entries with
  *              0 <= lo < hi <= N, or both NULL for the Balanced Distance
- *              Partitioning bands of length N (requires Hq <= N).  Keys with
- *              equal bands on all query heads of a key/value head are read
- *              once for all of them.
+ *              Partitioning bands of length N (requires Hq <= N).  Where the
+ *              query heads of every key/value head have equal bands, keys are
+ *              read once for all of them (above 16 rows, once for the largest
+ *              power of two that divides their number); otherwise once for each
  *   workspace: DEVICE buffer of spa_paged_attn_workspace_bytes(max_q, d)
  *              bytes, 256-byte aligned, caller-owned, overwritten; two calls
  *              that may overlap need two
