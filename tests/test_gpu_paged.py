@@ -559,3 +559,48 @@ def test_batch_padded_with_idle_sequences(spa, order):
     alone = Case(live, 64, 32, 32, 64, BF, "full", seed=13)
     alone.run(spa)
     assert median_ms(spa, c) < 6 * median_ms(spa, alone)
+
+
+def test_generation_captured_in_one_graph(spa):
+    # append and attention of one token per sequence, captured once and replayed
+    # while the lengths grow; then the same tokens as one prompt (the kernel for
+    # many rows).  Both are off by the tolerance above: |o| <= A <= max|v|
+    S, H, Hk, d, page, steps = 3, 8, 2, 64, 16, 50
+    kp = torch.full((60, Hk, page, d), float("nan"), dtype=BF, device=DEV)
+    vp = kp.clone()
+    table = torch.randperm(60, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(S, 20).to(DEV)
+    w, rope = torch.ones(d, device=DEV), spa.rope_table(320, d)
+    kv, x = torch.ones(S, dtype=torch.int32, device=DEV), torch.zeros(S, H + 2 * Hk, d, dtype=BF, device=DEV)
+    bands = dict(lo=[0] * H, hi=[320] * H, N=320)
+
+    def tokens(x, cu, n):
+        q, k, v = x.split([H, Hk, Hk], 1)
+        cu = torch.tensor(cu, dtype=torch.int32, device=DEV) if isinstance(cu, list) else cu
+        return spa.paged_attention(spa.paged_append(q, k, v, kp, vp, table, cu, kv, w, w, rope), kp, vp, table, cu, kv,
+                                   n, **bands)
+
+    cu = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    tokens(x, cu, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = tokens(x, cu, 1)
+    kp.fill_(float("nan"))
+    vp.fill_(float("nan"))
+    seen = torch.randn(steps, S, H + 2 * Hk, d, generator=torch.Generator().manual_seed(2)).to(BF).to(DEV)
+    got = []
+    for t in range(steps):
+        kv.fill_(t + 1)
+        x.copy_(seen[t])
+        graph.replay()
+        got.append((o.clone(), lse.clone()))
+    keys, values = kp.clone(), vp.clone()
+    kp.fill_(float("nan"))
+    vp.fill_(float("nan"))
+    o, lse = tokens(seen.transpose(0, 1).reshape(S * steps, -1, d), [0, steps, 2 * steps, 3 * steps], steps)
+    assert spa.spa_device_status() == spa.SPA_OK
+    for a, b in ((kp, keys), (vp, values)):  # one by one or together, the cache is the same
+        assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
+    far = 2 * (2 * HALF[BF] + 3e-5) * float(seen[:, :, H + Hk:].abs().max())
+    for t, (ot, lt) in enumerate(got):
+        assert float((o.view(S, steps, H, d)[:, t].float() - ot.float()).abs().max()) <= far
+        assert float((lse.view(S, steps, H)[:, t] - lt).abs().max()) <= 1e-4
