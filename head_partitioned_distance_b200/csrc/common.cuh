@@ -94,7 +94,14 @@ __device__ __forceinline__ int head_of(const int32_t* start, int H, int r) {
 // timeout outputs are incomplete, whatever a later call reports.
 __device__ int g_spa_status;
 
-__device__ __forceinline__ void report_status(int status) { atomicMax(&g_spa_status, status); }
+// (The highest code may always be stored and the lowest only over none: an
+// atomicMax for all, inlined in every wait, took 0.8 of 55.5 us more from a
+// 2048-token chunk of the paged attention.)
+__device__ __forceinline__ void report_status(int status) {
+  if (status == kStatusTimeout) atomicExch(&g_spa_status, kStatusTimeout);
+  else if (status == kStatusInval) atomicCAS(&g_spa_status, kStatusOk, kStatusInval);
+  else atomicMax(&g_spa_status, status);
+}
 
 // Sequences packed as token rows [cu_q[b], cu_q[b + 1]) of T that name rows
 // which do not exist: those are left out, and one thread of the grid says so.

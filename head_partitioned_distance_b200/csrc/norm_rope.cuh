@@ -428,7 +428,6 @@ __global__ void __launch_bounds__(kNrThreads) spa_paged_append_kernel(const __gr
     // a position without a table row or a page: nothing is cached for it
     if (slot < 0 && sub == 0) report_status(kStatusInval);
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_missing_rows(p.cu_q, p.B, p.T);
   const LaneColumns<NEIGHBOURS> lc(sub, p.rot);
   const HeadChunk hc(blockIdx.y, p.heads_per_group, p.Hq, p.Hk, p.Hk);
   const RowStrides rs = hc.kind == 0 ? p.qs : hc.kind == 1 ? p.ks : p.vs;
@@ -450,6 +449,7 @@ __global__ void __launch_bounds__(kNrThreads) spa_paged_append_kernel(const __gr
       if (store && hb + u < hc.h1) store_pairs(dst + (hb + u) * step, lc, out);
     }
   }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) report_missing_rows(p.cu_q, p.B, p.T);
 }
 
 }  // namespace spa

@@ -458,7 +458,6 @@ __global__ void __launch_bounds__(160, 2)
     PagedPages pages;
     int g = 0;
     bool ok = true;
-    if (blockIdx.x == 0 && lane == 0) report_missing_rows(p.cu_q, p.B, p.T);
     while (ok && w.next()) {
       if (lane == 0 && p.kv_len[w.it.b] > w.it.kv) report_status(kStatusInval);
       const int hk = w.it.hg / p.kv_div;
@@ -483,6 +482,8 @@ __global__ void __launch_bounds__(160, 2)
         __syncwarp();
       }
     }
+    // (here, where nothing waits for its loads)
+    if (blockIdx.x == 0 && lane == 0) report_missing_rows(p.cu_q, p.B, p.T);
     // every copy issued has landed before the CTA ends
     if (lane == 0)
       for (int s = 0; s < C::NS; ++s) {

@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(384, 1)
       RingSlot<C::NV> v;
       int nq[2] = {0, 0}, nk = 0, nv = 0;
       bool ok = true;
-      if (blockIdx.x == 0 && lane == 0) report_missing_rows(p.cu_q, p.B, p.T);
       while (ok && w.next()) {
         const PagedItem& it = w.it;
         const int hk = it.hg / p.kv_div;
@@ -354,6 +353,8 @@ __global__ void __launch_bounds__(384, 1)
           id_v = id;
         }
       }
+      // (here, where nothing waits for its loads)
+      if (blockIdx.x == 0 && lane == 0) report_missing_rows(p.cu_q, p.B, p.T);
       // Exit path: every load this warp issued has landed before the CTA ends.
       if (lane == 0) {
         for (int t = 0; t < 2; ++t)
