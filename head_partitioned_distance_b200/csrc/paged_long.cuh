@@ -23,8 +23,8 @@
 // special-function lanes), 1350 for the two products (2 x 512 of the tensor
 // core, and the signals between them), against which the other tile's step is
 // set.  4096 tokens of 32 heads over 16384 positions of one key/value head:
-// 1215 TFLOP/s, 74 % of the measured bf16 rate (1010-1100 over long calls, when
-// the power cap lowers the clocks).  Tried and slower there: 64-key
+// 1215 TFLOP/s, 74 % of the measured bf16 rate (8 key/value heads, in a loop
+// under the power cap: 970 to 1040).  Tried and slower there: 64-key
 // tiles with S ahead of the softmax (the issuing thread's own instructions
 // then take longer than the products: 970), a polynomial for part of the
 // exponentials (more instructions than it saves lanes: 1130 at a quarter), the
