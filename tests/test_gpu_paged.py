@@ -554,11 +554,13 @@ def test_batch_padded_with_idle_sequences(spa, order):
     c = Case(seqs, 64, 32, 32, 64, BF, "full", seed=13, pad=496)
     c.check(*c.run(spa))
     assert spa.spa_device_status() == spa.SPA_OK
-    # the idle places were 15872 items: stepping over each took 20 times as long
-    # as the attention
+    # the idle places are 15872 items: stepping over each, at 0.17 us, took 2.7 ms
+    # in the CTA they fell to.  As 496 sequences they cost the plan 16 us (1.5
+    # times the attention alone), and 0.3 us each (5.6 times) where one CTA's run
+    # goes across them
     alone = Case(live, 64, 32, 32, 64, BF, "full", seed=13)
     alone.run(spa)
-    assert median_ms(spa, c) < 6 * median_ms(spa, alone)
+    assert median_ms(spa, c) < (15 if order == "between" else 4) * median_ms(spa, alone)
 
 
 def test_generation_captured_in_one_graph(spa):
